@@ -49,6 +49,17 @@ EXPORTED = (
     # ssm_probe.h: issue-rate probes of single gfx950 units (no part of the gradient path)
     "ssm_probe_units",
     "ssm_probe_wall_clock_khz",
+    # ssm_linattn.h: linear attention with a decay for each head
+    "ssm_linattn_workspace_bytes",
+    "ssm_linattn_forward",
+    "ssm_linattn_grad",
+    "ssm_linattn_step",
+    # ssm_train.h: residual update with the norm, gradient clipping
+    "ssm_add_norm",
+    "ssm_add_norm_grad_workspace_bytes",
+    "ssm_add_norm_grad",
+    "ssm_clip_grads_workspace_bytes",
+    "ssm_clip_grads",
 )
 
 SSM_PROBE_FMA, SSM_PROBE_EXP, SSM_PROBE_EXP_FMA, SSM_PROBE_MFMA = 0, 1, 2, 3
@@ -520,3 +531,10 @@ def ssm_probe_wall_clock_khz() -> int:
     khz = ctypes.c_int(0)
     _check(lib.ssm_probe_wall_clock_khz(ctypes.byref(khz)), "ssm_probe_wall_clock_khz")
     return int(khz.value)
+
+
+# ---------------------------------------------------------------- operators (ssm_linattn.h, ssm_train.h)
+
+from .linattn import (LinattnDims, LinattnGrads, LinattnIn, linattn_forward, linattn_grad,  # noqa: E402
+                      linattn_step, linattn_workspace_bytes)
+from .train import add_norm, add_norm_grad, clip_grads  # noqa: E402

@@ -1,0 +1,12 @@
+// linattn_f32_128.hip -- the linear-attention kernels of io type f32 for q and k
+// heads padded to 128 channels.
+#include "linattn.inl"
+
+namespace la {
+
+hipError_t launch_f32_128(Kernel k, int dv, const Args& a, int nz, hipStream_t st) {
+  if (padded(dv) == 64) return launch_kind<float, 128, 64>(k, a, nz, st);
+  return launch_kind<float, 128, 128>(k, a, nz, st);
+}
+
+}  // namespace la
