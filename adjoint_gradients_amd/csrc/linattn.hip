@@ -219,6 +219,7 @@ using abi::good;
 using abi::good_or_null;
 
 constexpr int32_t kMaxHeads = 4096, kMaxSeqs = 65535;
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // a chunk's rows stay within 32-bit byte offsets
 constexpr int64_t kMaxStepRows = int64_t(1) << 22;
 
 size_t es(const ssm_linattn_dims* d) { return d->io == SSM_BF16 ? 2 : 4; }
@@ -234,7 +235,7 @@ ssm_status check_dims(const ssm_linattn_dims* d) {
 }
 
 bool good_ld(const ssm_linattn_dims* d, int64_t ld, int64_t row) {
-  return ld >= row && (ld * static_cast<int64_t>(es(d))) % 16 == 0 && ld <= (int64_t(1) << 40) / d->T;
+  return ld >= row && (ld * static_cast<int64_t>(es(d))) % 16 == 0 && ld <= kMaxLd;
 }
 
 ssm_status check_in(const ssm_linattn_dims* d, const ssm_linattn_in* in) {
@@ -344,6 +345,7 @@ Args base_args(const ssm_linattn_dims* d, const ssm_linattn_in* in, const Plan& 
   a.dkdv = d->dk * d->dv;
   a.log_decay = in->log_decay;
   a.ld_decay = d->decay_tokens ? d->Hv : 0;
+  a.sum_heads = d->Hk != d->Hv;
   return a;
 }
 
@@ -451,7 +453,6 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   rq.seg = w.seg[0];
   rq.sm = 1; rq.sn = d->dv;
   rq.out = w.part[0] ? static_cast<void*>(w.part[0]) : g->dq;
-  rq.out_f32 = w.part[0] ? 1 : 0;
   rq.ldo = part_ld;
   rq.tok = w.tok;
   rq.chunk_states = w.chunk_states;
@@ -469,7 +470,6 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   rk.seg = w.seg[1];
   rk.sm = 1; rk.sn = d->dv;
   rk.out = w.part[1] ? static_cast<void*>(w.part[1]) : g->dk;
-  rk.out_f32 = w.part[1] ? 1 : 0;
   rk.ldo = part_ld;
   rk.tok = w.tok;
   rk.chunk_states = w.chunk_states;

@@ -37,7 +37,6 @@ struct Run {
   float* s_end;                    // [S][Hv] the state leaving the sequences, or null
   int32_t sm, sn;                  // strides of a state's dm and dn index
   void* out;                       // token rows of Hv heads, or null
-  int32_t out_f32;                 // out is float32 whatever the io dtype
   float* tok;                      // [T][Hv] decay-gradient terms (written by the forward run, read by the reverse)
   float* chunk_states;             // [chunk slots][Hv][dm][dn] (padded) states entering each chunk
   float* dg_tok;                   // [T][Hv] decay gradient, or null
@@ -49,6 +48,7 @@ struct Args {
   int32_t Hv, dkdv;                // heads, floats of a state
   const float* log_decay;
   int64_t ld_decay;                // Hv, or 0 for one decay per head
+  int32_t sum_heads;               // dq and dk are float32, one per value head
   Run run[3];
 };
 

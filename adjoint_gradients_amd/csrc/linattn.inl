@@ -72,38 +72,36 @@ struct Cfg {
 template <class T, int DM, int DN, int MODE>
 struct Lds {
   using C = Cfg<T>;
+  static constexpr int PM = DM + C::EPV, PN = DN + C::EPV;
   static constexpr int q = 0;
-  static constexpr int k = q + (MODE == kAgg ? 0 : C::CH * DM * (int)sizeof(T));
-  static constexpr int v = k + C::CH * DM * (int)sizeof(T);
-  static constexpr int x = v + C::CH * DN * (int)sizeof(T);
-  static constexpr int p = x + (MODE == kOutFwdDg ? C::CH * DN * (int)sizeof(T) : 0);
+  static constexpr int k = q + (MODE == kAgg ? 0 : C::CH * PM * (int)sizeof(T));
+  static constexpr int v = k + C::CH * PM * (int)sizeof(T);
+  static constexpr int x = v + C::CH * PN * (int)sizeof(T);
+  static constexpr int p = x + (MODE == kOutFwdDg ? C::CH * PN * (int)sizeof(T) : 0);
   static constexpr int f = p + (MODE == kAgg ? 0 : C::CH * C::CH * (int)sizeof(T));
-  // two buffers of gh, gl, wq, wk; wc; then the decay gradient's partial sums
-  static constexpr int kDecay = 4 * C::CH;
-  static constexpr int wc = 2 * kDecay;
+  // gh, gl, wq; two buffers of wk and of wc; then the decay gradient's partial sums
+  static constexpr int wk = 3 * C::CH;
+  static constexpr int wc = wk + 2 * C::CH;
   static constexpr int red = wc + 4;
   static constexpr int floats = red + (MODE >= kOutFwdDg ? (4 + C::JW + C::NIB) * C::CH + 4 : 0);
   static constexpr int bytes = f + floats * 4;
 };
 
-// Element (r, c) of a tile of D columns in LDS.  A row's 16-byte chunks are
-// permuted by f(r), found from the three ways a tile is read: 16 rows at one
-// chunk (operand rows), 16 rows at half a chunk, and, transposing, rows 0-3
-// and 8-11 (bf16, two chunks each) or rows e, 4 + e, 8 + e, 12 + e (fp32, four
-// chunks each).  Each meets every bank equally often.
+// Element (r, c) of a tile of D columns in LDS.  Rows start 16 bytes later in
+// the banks than the row before: 16 rows read at one chunk of 16 bytes, or at
+// half a chunk, meet every bank equally often, and every address is one lane
+// offset plus a constant.  (The transposing reads meet half the banks twice;
+// a permutation of the chunks avoids that but needs an address of its own
+// for most reads, about a hundred registers.)
 template <class T, int D>
-__device__ __forceinline__ int at(int r, int c) {
+__device__ __forceinline__ int at(int r, int c) { return r * (D + Cfg<T>::EPV) + c; }
+
+// Element (i, j) of the scores, without padding (two workgroups a CU need the
+// space): a row's 16-byte chunks are permuted instead.
+template <class T>
+__device__ __forceinline__ int at_p(int i, int j) {
   constexpr int EPV = Cfg<T>::EPV;
-  int f;
-  if constexpr (D * sizeof(T) == 128) {
-    if constexpr (Cfg<T>::kBf) f = (r & 2) | ((r >> 1) & 4) | ((r >> 2) & 1);
-    else f = (r >> 1) & 7;
-  } else if constexpr (Cfg<T>::kBf) {
-    f = ((r & 3) << 1) | (r & 8) | ((r >> 2) & 1);
-  } else {
-    f = r & 15;
-  }
-  return r * D + ((c / EPV) ^ f) * EPV + c % EPV;
+  return i * Cfg<T>::CH + ((j / EPV) ^ ((i >> 1) & 7)) * EPV + j % EPV;
 }
 
 struct Segment {
@@ -146,12 +144,40 @@ __device__ __forceinline__ bool find_segment(const Seqs& sq, uint32_t slot, int 
   return true;
 }
 
+// Barrier that orders LDS accesses only.  The fence of __syncthreads() also
+// waits for every global access in flight, which here are the next chunk's
+// loads and the previous one's stores.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // 2^x of a 64-bit x, to fp32 accuracy also for large |x|.
 __device__ __forceinline__ float exp2_split(double x) {
   const float h = static_cast<float>(x);
   const float l = static_cast<float>(x - static_cast<double>(h));
   const float e = ssm::fast_exp2(h);
   return fmaf(e, l * kLn2, e);
+}
+
+// A 64-bit value moved across lanes by a DPP control; lanes without a source
+// (or outside the row mask) get 0.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  const uint2 r{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u.x), CTRL, ROWS, 0xF, true)),
+                static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u.y), CTRL, ROWS, 0xF, true))};
+  return __builtin_bit_cast(double, r);
+}
+
+// Inclusive sums over the lanes up to this one: inside rows of 16 lanes by
+// shifts of 1, 2, 4, 8, then across rows by the broadcasts of lane 15 of each
+// row to the next one and of lane 31 to the upper half.
+__device__ __forceinline__ double prefix_sum(double v) {
+  v += dpp_or_zero<0x111, 0xF>(v);
+  v += dpp_or_zero<0x112, 0xF>(v);
+  v += dpp_or_zero<0x114, 0xF>(v);
+  v += dpp_or_zero<0x118, 0xF>(v);
+  v += dpp_or_zero<0x142, 0xA>(v);
+  v += dpp_or_zero<0x143, 0xC>(v);
+  return v;
 }
 
 template <int D>
@@ -201,33 +227,68 @@ __device__ __forceinline__ bf16x8_t read_tr(bf16_t* tile, int t0, int c0, int l1
   return __builtin_bit_cast(bf16x8_t, p);
 }
 
-// A CH x D tile: global rows -> registers -> LDS.  Rows past nv and channels
-// past d are zero.
+// Rows of d elements, ld apart, from a chunk's first token on; accesses past
+// row nv read zero and store nothing (offsets are range-checked in hardware,
+// so no lane mask or branch splits the loads).  A null base is an empty range.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t ld, int nv, int d, int es) {
+  const int bytes = p && nv > 0 ? static_cast<int>(((nv - 1) * ld + d) * es) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, ssm::kBufWord3);
+}
+
+// Byte offset past any row range (which holds at most 64 x 2^24 bytes).
+constexpr uint32_t kOutside = ssm::kBufOutside;
+
+// A CH x D tile: global rows -> registers -> LDS.  Rows past the last token
+// and channels past d are zero.
 template <class T, int D>
 struct Tile {
   using C = Cfg<T>;
   static constexpr int N = C::CH * D / C::EPV / kThreads;
-  uint4 r[N];
+  static constexpr int RPI = kThreads / (D / C::EPV);  // rows a load instruction covers
+  typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
+  u32x4 r[N];
+  uint32_t voff, step;  // the lane's byte offset; bytes between the rows of successive instructions
+  int lds_off;
+  __device__ __forceinline__ void init(int64_t ld, int d) {
+    const int row = threadIdx.x / (D / C::EPV), col = threadIdx.x % (D / C::EPV) * C::EPV;
+    voff = col < d ? static_cast<uint32_t>((row * ld + col) * sizeof(T)) : kOutside;
+    step = static_cast<uint32_t>(RPI * ld * sizeof(T));
+    lds_off = at<T, D>(row, col);
+  }
   __device__ __forceinline__ void load(const T* p, int64_t ld, int nv, int d) {
+    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p, ld, nv, d, sizeof(T));
 #pragma unroll
     for (int i = 0; i < N; i++) {
-      const int idx = threadIdx.x + kThreads * i;
-      const int row = idx / (D / C::EPV), col = idx % (D / C::EPV) * C::EPV;
-      r[i] = uint4{0, 0, 0, 0};
-      if (row < nv && col < d) r[i] = *reinterpret_cast<const uint4*>(p + row * ld + col);
+      // a lane past d stays outside: steps stay under 2^30 bytes in all
+      r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff + i * step, 0, 0));
     }
   }
   __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      const int idx = threadIdx.x + kThreads * i;
-      const int row = idx / (D / C::EPV), col = idx % (D / C::EPV) * C::EPV;
-      *reinterpret_cast<uint4*>(lds + at<T, D>(row, col)) = r[i];
-    }
+    for (int i = 0; i < N; i++) *reinterpret_cast<u32x4*>(lds + lds_off + at<T, D>(i * RPI, 0)) = r[i];
   }
 };
 
-template <class T, int DM, int DN, bool REV, int MODE>
+// Four output elements at a byte offset of a row range.
+__device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, f32x4_t v, float*) {
+  __builtin_amdgcn_raw_buffer_store_b128(
+      __builtin_bit_cast(__attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t, v), rs, voff, 0, 0);
+}
+__device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, f32x4_t v, bf16_t*) {
+  typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, rs, voff, 0, 0);
+}
+__device__ __forceinline__ f32x4_t load_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, const float*) {
+  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0));
+}
+__device__ __forceinline__ f32x4_t load_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, const bf16_t*) {
+  const auto u = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, 0, 0);
+  return f32x4_t{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
+                 __uint_as_float(u[1] & 0xffff0000u)};
+}
+
+// OT: type of the output rows, the io type or float.
+template <class T, class OT, int DM, int DN, bool REV, int MODE>
 __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
   using C = Cfg<T>;
   using M = Lds<T, DM, DN, MODE>;
@@ -237,7 +298,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
   constexpr bool kDg = MODE >= kOutFwdDg;
   constexpr int kDecayWave = REV ? 3 : 0;  // the wavefront with the fewest score blocks
 
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int l15 = lane & 15, g = lane >> 4;
   const int h = blockIdx.y;
   const uint32_t slot = blockIdx.x;
@@ -292,65 +353,117 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 
   Tile<T, DM> tq, tk;
   Tile<T, DN> tv, tx;
-  float gl_next = 0.0f;  // this lane's log decay of the chunk being loaded
-  auto issue = [&](int c) {
-    const int64_t tb = sg.t0 + c * CH;
-    const int nv = sg.t1 - static_cast<int>(tb);
-    if constexpr (MODE != kAgg) tq.load(Qp + tb * r.ldq, r.ldq, nv, r.dm);
-    tk.load(Kp + tb * r.ldk, r.ldk, nv, r.dm);
-    tv.load(Vp + tb * r.ldv, r.ldv, nv, r.dn);
-    if constexpr (MODE == kOutFwdDg) tx.load(Xp + tb * r.ldx, r.ldx, nv, r.dn);
-    if (wave == kDecayWave) {
-      gl_next = 0.0f;
-      if (lane < CH && lane < nv) gl_next = a.log_decay[(tb + lane) * a.ld_decay + h];
-    }
+  if constexpr (MODE != kAgg) tq.init(r.ldq, r.dm);
+  tk.init(r.ldk, r.dm);
+  tv.init(r.ldv, r.dn);
+  if constexpr (MODE == kOutFwdDg) tx.init(r.ldx, r.dn);
+  constexpr int es_out = sizeof(OT);
+  float g_next;  // this lane's log decay of the chunk being loaded
+  // Loads of chunk c into registers; past the segment's end (the walk's last
+  // step) the ranges are empty and nothing is fetched.
+  auto chunk_rows = [&](int c, bool live) {
+    const int nv = live ? sg.t1 - (sg.t0 + c * CH) : 0;
+    return nv < CH ? nv : CH;
+  };
+  auto issue_decay = [&](int c, bool live) {
+    const int64_t tb = sg.t0 + (live ? c * CH : 0);
+    const int n = chunk_rows(c, live);
+    const __amdgpu_buffer_rsrc_t rg = rows_rsrc(a.log_decay + tb * a.ld_decay + h, a.ld_decay, n, 1, 4);
+    g_next = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rg, lane < n ? lane * static_cast<uint32_t>(a.ld_decay) * 4u : kOutside, 0, 0));
+  };
+  auto issue = [&](int c, bool live) {
+    const int64_t tb = sg.t0 + (live ? c * CH : 0);
+    const int n = chunk_rows(c, live);
+    if constexpr (MODE != kAgg) tq.load(Qp + tb * r.ldq, r.ldq, n, r.dm);
+    tk.load(Kp + tb * r.ldk, r.ldk, n, r.dm);
+    tv.load(Vp + tb * r.ldv, r.ldv, n, r.dn);
+    if constexpr (MODE == kOutFwdDg) tx.load(Xp + tb * r.ldx, r.ldx, n, r.dn);
   };
   // Sums of a chunk's log decays in 64 bits (base 2) and the weights made
-  // from them.  A decay below 2^-20000 is taken as 2^-20000: both are zero
-  // in every product, and -inf would make 0 of inf - inf.
+  // from them.  A decay below e^-13000 is taken as that: both are zero in
+  // every product, and -inf would make a NaN of inf - inf.
   auto decays = [&](int buf) {
-    double G = static_cast<double>(gl_next < -13000.0f ? -13000.0f : gl_next) * 1.4426950408889634;
-#pragma unroll
-    for (int d = 1; d < CH; d <<= 1) {
-      const double u = __shfl_up(G, d, 64);
-      if (lane >= d) G += u;
-    }
-    const double tot = __shfl(G, CH - 1, 64);
-    float* o = sF + buf * M::kDecay;
+    const double G =
+        prefix_sum(static_cast<double>(g_next < -13000.0f ? -13000.0f : g_next) * 1.4426950408889634);
+    const uint2 gb = __builtin_bit_cast(uint2, G);
+    const uint2 tb{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.x), CH - 1)),
+                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.y), CH - 1))};
+    const double tot = __builtin_bit_cast(double, tb);
     if (lane < CH) {
       const float hi = static_cast<float>(G);
-      o[lane] = hi;
-      o[CH + lane] = static_cast<float>(G - static_cast<double>(hi));
+      sF[lane] = hi;
+      sF[CH + lane] = static_cast<float>(G - static_cast<double>(hi));
       const float eg = exp2_split(G), er = exp2_split(tot - G);
-      o[2 * CH + lane] = r.qs * (REV ? er : eg);
-      o[3 * CH + lane] = r.ks * (REV ? eg : er);
+      sF[2 * CH + lane] = r.qs * (REV ? er : eg);
+      sF[M::wk + buf * CH + lane] = r.ks * (REV ? eg : er);
     }
     if (lane == 0) sF[M::wc + buf] = exp2_split(tot);
+  };
+
+  auto chunk_state = [&](int c) {
+    return reinterpret_cast<f32x4_t*>(r.chunk_states +
+                                      (static_cast<int64_t>(sg.chunk_slot + c) * a.Hv + h) * (DM * DN));
   };
 
   float decay_seg = 1.0f;
   double dg_sum = 0.0;
   if (nch > 0) {
-    issue(REV ? nch - 1 : 0);
+    issue_decay(REV ? nch - 1 : 0, true);
+    issue(REV ? nch - 1 : 0, true);
     if (wave == kDecayWave) decays(0);
+    // Global accesses retire in order: the loop waits for its loads by
+    // counting what it issued after them.  Wait for the entering state and
+    // issue as many (empty) stores here as a turn does, so that the first
+    // turn counts like the others and no turn waits for its predecessor's
+    // stores.
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
+    if constexpr (MODE != kAgg) {
+      const __amdgpu_buffer_rsrc_t none = rows_rsrc(nullptr, 0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < NB * NIB; i++) store_rows(none, 16 * lane, f32x4_t{0.f, 0.f, 0.f, 0.f}, static_cast<OT*>(nullptr));
+      if constexpr (MODE == kOutFwdDg)
+#pragma unroll
+        for (int i = 0; i < MB * NB; i++) store_rows(none, 16 * lane, f32x4_t{0.f, 0.f, 0.f, 0.f}, static_cast<float*>(nullptr));
+    }
   }
   for (int it = 0; it < nch; it++) {
     const int c = REV ? nch - 1 - it : it;
     const int64_t tb = sg.t0 + static_cast<int64_t>(c) * CH;
     const int nv = sg.t1 - static_cast<int>(tb) < CH ? sg.t1 - static_cast<int>(tb) : CH;
     const int buf = it & 1;
-    const float* const gh = sF + buf * M::kDecay;
-    const float* const gl = gh + CH;
-    const float* const wq = gh + 2 * CH;
-    const float* const wk = gh + 3 * CH;
+    const float* const gh = sF;
+    const float* const gl = sF + CH;
+    const float* const wq = sF + 2 * CH;
+    const float* const wk = sF + M::wk + buf * CH;
 
-    if (it > 0) __syncthreads();  // the previous chunk's readers are done
+    if (it > 0) lds_barrier();  // the previous chunk's readers are done
     if constexpr (MODE != kAgg) tq.store(sQ);
     tk.store(sK);
     tv.store(sV);
     if constexpr (MODE == kOutFwdDg) tx.store(sX);
-    __syncthreads();
-    if (it + 1 < nch) issue(REV ? c - 1 : c + 1);
+    lds_barrier();
+    // this chunk's own waits come first in program order: the next chunk's
+    // decays, and the loads that only this chunk uses
+    issue_decay(REV ? c - 1 : c + 1, it + 1 < nch);
+    f32x4_t cs[MODE == kOutRevDg ? MB : 1][MODE == kOutRevDg ? NB : 1], xv[MODE == kOutRevDg ? NB : 1][MODE == kOutRevDg ? NIB : 1];
+    if constexpr (MODE == kOutRevDg) {
+      const f32x4_t* p = chunk_state(c);
+#pragma unroll
+      for (int mb = 0; mb < MB; mb++)
+#pragma unroll
+        for (int nb = 0; nb < NB; nb++) cs[mb][nb] = p[(mb * NB + nb) * kThreads + threadIdx.x];
+      const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + tb * r.ldx, r.ldx, nv, r.dn, sizeof(T));
+#pragma unroll
+      for (int nb = 0; nb < NB; nb++) {
+        const int n = n0 + 16 * nb + 4 * g;
+        const uint32_t vo = n < r.dn ? static_cast<uint32_t>((l15 * r.ldx + n) * sizeof(T)) : kOutside;
+#pragma unroll
+        for (int b = 0; b < NIB; b++) xv[nb][b] = load_rows(rx, vo + b * static_cast<uint32_t>(16 * r.ldx * sizeof(T)), Xp);
+      }
+    } else {
+      issue(REV ? c - 1 : c + 1, it + 1 < nch);
+    }
     const float wc = sF[M::wc + buf];
 
     f32x4_t Y[NB][NIB];
@@ -412,7 +525,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
             }
           }
         }
-        store4(sP + at<T, CH>(i, 16 * jb + 4 * g), p);
+        store4(sP + at_p<T>(i, 16 * jb + 4 * g), p);
         if constexpr (MODE == kOutFwdDg) {
 #pragma unroll
           for (int e = 0; e < 4; e++) {
@@ -424,6 +537,20 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
       if constexpr (MODE == kOutFwdDg) {
         rowsum = sum_groups(rowsum);
         if (g == 0) sRow[(wave / NIB) * CH + i] = rowsum;
+      }
+
+      if constexpr (MODE == kOutRevDg) {
+        // the state entering this chunk meets the adjoint of the one leaving it
+        float dot = 0.0f;
+#pragma unroll
+        for (int mb = 0; mb < MB; mb++)
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) dot = fmaf(cs[mb][nb][e], S[mb][nb][e], dot);
+        dot = sum_groups(sum16(dot));
+        if (lane == 0) sDot[wave] = dot;
+        issue(REV ? c - 1 : c + 1, it + 1 < nch);
       }
 
       // the state's part, transposed: rows n of this wavefront, columns i
@@ -482,12 +609,9 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
             for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
           }
           if constexpr (MODE == kOutRevDg) {
-            const int n = n0 + 16 * nb + 4 * g, i2 = 16 * b + l15;
-            if (i2 < nv && n < r.dn) {
-              const f32x4_t x = load4(Xp + (tb + i2) * r.ldx + n);
+            const f32x4_t x = xv[nb][b];
 #pragma unroll
-              for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
-            }
+            for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
           }
         }
         if constexpr (kDg) {
@@ -495,33 +619,17 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
           if (g == 0) sRint[wave * CH + 16 * b + l15] = dot;
         }
       }
-      if constexpr (kDg) {
-        // the state entering this chunk: kept by the forward run, met by the
-        // reverse run's adjoint of the state leaving it
-        f32x4_t* cs = reinterpret_cast<f32x4_t*>(
-            r.chunk_states + (static_cast<int64_t>(sg.chunk_slot + c) * a.Hv + h) * (DM * DN));
-        float dot = 0.0f;
+      if constexpr (MODE == kOutFwdDg) {
+        // the state entering this chunk, for the reverse run
+        f32x4_t* p = chunk_state(c);
 #pragma unroll
         for (int mb = 0; mb < MB; mb++)
 #pragma unroll
-          for (int nb = 0; nb < NB; nb++) {
-            f32x4_t* p = cs + (mb * NB + nb) * kThreads + threadIdx.x;
-            if constexpr (MODE == kOutFwdDg) {
-              *p = S[mb][nb];
-            } else {
-              const f32x4_t s = *p;
-#pragma unroll
-              for (int e = 0; e < 4; e++) dot = fmaf(s[e], S[mb][nb][e], dot);
-            }
-          }
-        if constexpr (MODE == kOutRevDg) {
-          dot = sum_groups(sum16(dot));
-          if (lane == 0) sDot[wave] = dot;
-        }
+          for (int nb = 0; nb < NB; nb++) p[(mb * NB + nb) * kThreads + threadIdx.x] = S[mb][nb];
       }
     }
+    if constexpr (MODE != kAgg) lds_barrier();  // scores and partial sums are in LDS; gh, gl, wq are free
     if (wave == kDecayWave && it + 1 < nch) decays(buf ^ 1);
-    if constexpr (MODE != kAgg) __syncthreads();  // scores and partial sums are in LDS
 
     // V of this wavefront's columns, tokens along the lane's elements
     if constexpr (kBf) {
@@ -538,7 +646,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 #pragma unroll
           for (int kb = 0; kb < CH / 32; kb++)
             if (REV ? 2 * kb + 1 >= b : 2 * kb <= b) {
-              const bf16x8_t pf = load8(sP + at<T, CH>(16 * b + l15, 32 * kb + 8 * g));
+              const bf16x8_t pf = load8(sP + at_p<T>(16 * b + l15, 32 * kb + 8 * g));
 #pragma unroll
               for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
             }
@@ -587,7 +695,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 #pragma unroll
           for (int b = 0; b < NIB; b++)
             if (REV ? tk16 >= b : tk16 <= b) {
-              const f32x4_t p = load4(sP + at<T, CH>(16 * b + l15, 16 * tk16 + 4 * g));
+              const f32x4_t p = load4(sP + at_p<T>(16 * b + l15, 16 * tk16 + 4 * g));
 #pragma unroll
               for (int nb = 0; nb < NB; nb++)
 #pragma unroll
@@ -608,16 +716,18 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
     if constexpr (MODE == kAgg) decay_seg *= wc;
 
     if constexpr (MODE != kAgg) {
-#pragma unroll
-      for (int b = 0; b < NIB; b++) {
-        const int i = 16 * b + l15;
+      {
+        const int64_t o0 = tb * r.ldo + h * r.dn;
+        char* const ob = r.out ? static_cast<char*>(r.out) + o0 * es_out : nullptr;
+        const __amdgpu_buffer_rsrc_t ro = rows_rsrc(ob, r.ldo, nv, r.dn, es_out);
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
           const int n = n0 + 16 * nb + 4 * g;
-          if (r.out && i < nv && n < r.dn) {
-            const int64_t o = (tb + i) * r.ldo + h * r.dn + n;
-            if (r.out_f32) store4(static_cast<float*>(r.out) + o, Y[nb][b]);
-            else store4(static_cast<T*>(r.out) + o, Y[nb][b]);
+          const uint32_t vo = n < r.dn ? static_cast<uint32_t>((l15 * r.ldo + n) * es_out) : kOutside;
+#pragma unroll
+          for (int b = 0; b < NIB; b++) {
+            const uint32_t v = vo + b * static_cast<uint32_t>(16 * r.ldo * es_out);
+            store_rows(ro, v, Y[nb][b], static_cast<OT*>(nullptr));
           }
         }
       }
@@ -643,13 +753,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
             if (lane < nv) r.tok[o] = static_cast<float>(x);
           } else {
             // sums over j < t
-            const double own = x;
-#pragma unroll
-            for (int d = 1; d < CH; d <<= 1) {
-              const double u = __shfl_up(x, d, 64);
-              if (lane >= d) x += u;
-            }
-            x -= own;
+            x = prefix_sum(x) - x;
             if (lane < nv) {
               const float dot = (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]);
               const double dg = x + static_cast<double>(wc * dot) + static_cast<double>(r.tok[o]);
@@ -690,23 +794,25 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
   }
 }
 
-template <class T, int DK, int DV, int KIND>
+// Kinds: kGrad... with PT the type of dq and dk, float where the value heads
+// of a key head are summed afterwards.
+template <class T, class PT, int DK, int DV, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void k_linattn(Args a) {
   extern __shared__ __attribute__((aligned(16))) char smem_la[];
   if constexpr (KIND == kForward) {
-    run<T, DK, DV, false, kOut>(a, a.run[0], smem_la);
+    run<T, T, DK, DV, false, kOut>(a, a.run[0], smem_la);
   } else if constexpr (KIND == kAggregate) {
-    if (blockIdx.z == 0) run<T, DK, DV, false, kAgg>(a, a.run[0], smem_la);
-    else run<T, DK, DV, true, kAgg>(a, a.run[1], smem_la);
+    if (blockIdx.z == 0) run<T, T, DK, DV, false, kAgg>(a, a.run[0], smem_la);
+    else run<T, T, DK, DV, true, kAgg>(a, a.run[1], smem_la);
   } else if constexpr (KIND == kGradFirst) {
-    if (blockIdx.z == 0) run<T, DV, DK, false, kOutFwdDg>(a, a.run[0], smem_la);
-    else run<T, DK, DV, true, kOut>(a, a.run[1], smem_la);
+    if (blockIdx.z == 0) run<T, PT, DV, DK, false, kOutFwdDg>(a, a.run[0], smem_la);
+    else run<T, T, DK, DV, true, kOut>(a, a.run[1], smem_la);
   } else if constexpr (KIND == kGradSecond) {
-    run<T, DV, DK, true, kOutRevDg>(a, a.run[0], smem_la);
+    run<T, PT, DV, DK, true, kOutRevDg>(a, a.run[0], smem_la);
   } else {
-    if (blockIdx.z == 0) run<T, DV, DK, false, kOut>(a, a.run[0], smem_la);
-    else if (blockIdx.z == 1) run<T, DK, DV, true, kOut>(a, a.run[1], smem_la);
-    else run<T, DV, DK, true, kOut>(a, a.run[2], smem_la);
+    if (blockIdx.z == 0) run<T, PT, DV, DK, false, kOut>(a, a.run[0], smem_la);
+    else if (blockIdx.z == 1) run<T, T, DK, DV, true, kOut>(a, a.run[1], smem_la);
+    else run<T, PT, DV, DK, true, kOut>(a, a.run[2], smem_la);
   }
 }
 
@@ -721,11 +827,11 @@ constexpr int lds_bytes() {
   return max2(Lds<T, DV, DK, kOut>::bytes, Lds<T, DK, DV, kOut>::bytes);
 }
 
-template <class T, int DK, int DV, int KIND>
+template <class T, class PT, int DK, int DV, int KIND>
 hipError_t launch_one(const Args& a, int nz, hipStream_t st) {
   constexpr int lds = lds_bytes<T, DK, DV, KIND>();
   static_assert(lds <= 80 * 1024, "two workgroups share a CU's 160 KB");
-  auto kern = k_linattn<T, DK, DV, KIND>;
+  auto kern = k_linattn<T, PT, DK, DV, KIND>;
   hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   const dim3 grid(static_cast<unsigned>(slot_count(a.sq.T, a.sq.S, a.sq.L)), static_cast<unsigned>(a.Hv),
@@ -734,16 +840,19 @@ hipError_t launch_one(const Args& a, int nz, hipStream_t st) {
   return hipGetLastError();
 }
 
+template <class T, class PT, int DK, int DV>
+hipError_t launch_grad(Kernel k, const Args& a, int nz, hipStream_t st) {
+  if (k == kGradFirst) return launch_one<T, PT, DK, DV, kGradFirst>(a, nz, st);
+  if (k == kGradSecond) return launch_one<T, PT, DK, DV, kGradSecond>(a, nz, st);
+  return launch_one<T, PT, DK, DV, kGradPlain>(a, nz, st);
+}
+
 template <class T, int DK, int DV>
 hipError_t launch_kind(Kernel k, const Args& a, int nz, hipStream_t st) {
-  switch (k) {
-    case kForward: return launch_one<T, DK, DV, kForward>(a, nz, st);
-    case kAggregate: return launch_one<T, DK, DV, kAggregate>(a, nz, st);
-    case kGradFirst: return launch_one<T, DK, DV, kGradFirst>(a, nz, st);
-    case kGradSecond: return launch_one<T, DK, DV, kGradSecond>(a, nz, st);
-    case kGradPlain: return launch_one<T, DK, DV, kGradPlain>(a, nz, st);
-  }
-  return hipErrorInvalidValue;
+  if (k == kForward) return launch_one<T, T, DK, DV, kForward>(a, nz, st);
+  if (k == kAggregate) return launch_one<T, T, DK, DV, kAggregate>(a, nz, st);
+  if (a.sum_heads) return launch_grad<T, float, DK, DV>(k, a, nz, st);
+  return launch_grad<T, T, DK, DV>(k, a, nz, st);
 }
 
 }  // namespace

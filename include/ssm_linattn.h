@@ -24,7 +24,7 @@
  *
  * Layouts (row-major, elements): q, k [T][Hk][dk], v, y, dy [T][Hv][dv] in the
  * io dtype, dq, dk, dv likewise; a row of q, k, v, y, dy starts ld elements
- * after the one before it (ld >= heads * d, ld a multiple of 16 bytes).
+ * after the one before it (heads * d <= ld <= 2^22, ld a multiple of 16 bytes).
  * log_decay and its gradient [T][Hv] or [Hv], states [S][Hv][dk][dv], float32.
  *
  * Supported: dk and dv multiples of 8 up to 128, Hk divides Hv, Hv <= 4096,
