@@ -832,8 +832,11 @@ hipError_t launch_one(const Args& a, int nz, hipStream_t st) {
   constexpr int lds = lds_bytes<T, DK, DV, KIND>();
   static_assert(lds <= 80 * 1024, "two workgroups share a CU's 160 KB");
   auto kern = k_linattn<T, PT, DK, DV, KIND>;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-  if (e != hipSuccess) return e;
+  if constexpr (lds > 64 * 1024) {
+    const hipError_t e =
+        hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
   const dim3 grid(static_cast<unsigned>(slot_count(a.sq.T, a.sq.S, a.sq.L)), static_cast<unsigned>(a.Hv),
                   static_cast<unsigned>(nz));
   kern<<<grid, kThreads, lds, st>>>(a);

@@ -54,62 +54,64 @@ for _f in (lib.ssm_linattn_workspace_bytes, lib.ssm_linattn_forward, lib.ssm_lin
 GRADS = ("dq", "dk", "dv", "dlog_decay", "dh0")
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _bad(msg: str):
     raise SsmError(1, msg)
 
 
 @contextlib.contextmanager
-def _foreign(device, stream):
-    """The given stream, or another device's current one, for the duration of a call."""
-    if stream is not None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)):
-            yield int(stream)
-    else:
+def _on(device, stream):
+    """Makes a tensor's device, and the raw stream handle if given, current."""
+    if stream is None:
         with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-
-
-def _context(device, stream):
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(torch.cuda.current_stream(device).cuda_stream)
-    return _foreign(device, stream)
+            yield
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device)):
+            yield
 
 
 def _gpu(t, name: str, device=None, dtype=None):
+    """Refuses anything but a GPU tensor (of this device index and dtype); returns its device index."""
     if not isinstance(t, torch.Tensor):
         _bad(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if not t.is_cuda:
+    d = t.get_device()
+    if d < 0:
         _bad(f"{name}: must be a GPU tensor (got {t.device})")
-    if device is not None and t.device != device:
-        _bad(f"{name}: on {t.device}, the other tensors on {device}")
-    if dtype is not None and t.dtype != dtype:
+    if device is not None and d != device:
+        _bad(f"{name}: on {t.device}, other tensors of the call on cuda:{device}")
+    if dtype is not None and t.dtype is not dtype:
         _bad(f"{name}: dtype {t.dtype}, expected {dtype}")
+    return d
 
 
 def _dense(t, name: str, shape, device, dtype):
-    """A contiguous tensor of this shape, or None."""
+    """The address of a contiguous tensor of this shape; None for None."""
     if t is None:
         return None
     _gpu(t, name, device, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         _bad(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         _bad(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _rows(t, name: str, lead, device, dtype, H=None, d=None):
-    """Token rows [*lead, H, d] with contiguous heads and channels: (H, d, elements between rows)."""
+def _rows(t, name: str, lead, device, dtype, heads=None):
+    """Token rows [*lead, H, d] with contiguous heads and channels: ((H, d), elements between rows)."""
     _gpu(t, name, device, dtype)
     shape = t.shape
     n = len(lead)
-    if len(shape) != n + 2 or tuple(shape[:n]) != tuple(lead):
+    if len(shape) != n + 2 or shape[:n] != lead:
         _bad(f"{name}: shape {tuple(shape)}, expected {tuple(lead)} rows of heads and channels")
-    h, c = shape[n], shape[n + 1]
-    if (H is not None and h != H) or (d is not None and c != d):
-        _bad(f"{name}: {h} heads of {c} channels, expected {H} of {d}")
-    if h < 1 or c < 1:
-        _bad(f"{name}: empty heads")
+    hd = shape[n:]
+    if heads is not None and hd != heads:
+        _bad(f"{name}: {hd[0]} heads of {hd[1]} channels, expected {heads[0]} of {heads[1]}")
+    h, c = hd
+    if t.is_contiguous():
+        return hd, h * c
     st = t.stride()
     if (c > 1 and st[n + 1] != 1) or (h > 1 and st[n] != c):
         _bad(f"{name}: heads and channels must be contiguous (strides {st})")
@@ -117,40 +119,38 @@ def _rows(t, name: str, lead, device, dtype, H=None, d=None):
     ld = st[n - 1] if rows > 1 else st[0] if n == 2 and shape[0] > 1 else h * c
     if n == 2 and shape[0] > 1 and st[0] != rows * ld:
         _bad(f"{name}: sequences must follow one another (strides {st})")
-    return h, c, ld
+    return hd, ld
 
 
-def _setup(q, k, v, log_decay, scale, seq_start, step=False):
-    """Checks the inputs; returns (dims, device, leading shape, LinattnIn)."""
-    _gpu(q, "q")
-    device, io = q.device, q.dtype
+def _setup(q, k, v, log_decay, scale, seq_start, device, step=False):
+    """Checks the inputs; returns (dims, leading shape, v's heads, LinattnIn)."""
+    io = q.dtype
     if io not in _IO:
         _bad(f"q: dtype {io}, expected bfloat16 or float32")
-    if q.dim() not in ((3,) if step else (3, 4)):
-        _bad(f"q: {q.dim()} dimensions")
-    lead = tuple(q.shape[:-2])
-    Hk, dk, ldq = _rows(q, "q", lead, device, io)
-    _, _, ldk = _rows(k, "k", lead, device, io, Hk, dk)
-    Hv, dv, ldv = _rows(v, "v", lead, device, io)
-    T = 1
-    for n in lead:
-        T *= n
-    if T < 1:
-        _bad("no tokens")
-    S, starts = (lead[0] if len(lead) == 2 else 1), None
+    nd = q.dim()
+    if nd != 3 and (nd != 4 or step):
+        _bad(f"q: {nd} dimensions")
+    lead = q.shape[:-2]
+    hk, ldq = _rows(q, "q", lead, device, io)
+    _, ldk = _rows(k, "k", lead, device, io, hk)
+    hv, ldv = _rows(v, "v", lead, device, io)
+    T, S, starts = q.shape[0], 1, None
+    if nd == 4:
+        S, T = T, T * q.shape[1]
+    if T < 1 or hk[0] < 1 or hv[0] < 1:
+        _bad("no tokens or no heads")
     if seq_start is not None:
-        if len(lead) != 1:
+        if nd != 3:
             _bad("seq_start goes with packed tokens [T, H, d]")
         S = seq_start.numel() - 1 if isinstance(seq_start, torch.Tensor) else 0
         if S < 1:
-            _bad("seq_start: an int32 tensor of at least two offsets")
+            _bad("seq_start: expected an int32 tensor of at least two offsets")
         starts = _dense(seq_start, "seq_start", (S + 1,), device, torch.int32)
     _gpu(log_decay, "log_decay", device, torch.float32)
     tokens = log_decay.dim() != 1
-    _dense(log_decay, "log_decay", lead + (Hv,) if tokens else (Hv,), device, torch.float32)
-    dims = LinattnDims(T, S, Hk, Hv, dk, dv, _IO[io], 1 if tokens else 0, float(scale))
-    ins = LinattnIn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, log_decay.data_ptr(), starts, None)
-    return dims, device, lead, ins
+    g = _dense(log_decay, "log_decay", lead + hv[:1] if tokens else hv[:1], device, torch.float32)
+    dims = LinattnDims(T, S, hk[0], hv[0], hk[1], hv[1], _IO[io], 1 if tokens else 0, scale)
+    return dims, lead, hv, LinattnIn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, g, starts, None)
 
 
 def linattn_workspace_bytes(dims: LinattnDims, grads: LinattnGrads | None = None) -> int:
@@ -163,11 +163,15 @@ def linattn_workspace_bytes(dims: LinattnDims, grads: LinattnGrads | None = None
 
 def _workspace(ws, nbytes: int, device):
     if ws is None:
-        return alloc_workspace(nbytes, device) if nbytes else None
+        return alloc_workspace(nbytes, f"cuda:{device}") if nbytes else None
     _gpu(ws, "workspace", device, torch.uint8)
     if not ws.is_contiguous() or ws.numel() < nbytes:
         raise SsmError(2, f"workspace: {nbytes} contiguous bytes needed")
     return ws
+
+
+def _ws_args(w):
+    return (None, 0) if w is None else (w.data_ptr(), w.numel())
 
 
 def linattn_forward(q, k, v, log_decay, seq_start=None, h0=None, scale=1.0, want_state=False, y=None, hT=None,
@@ -175,20 +179,24 @@ def linattn_forward(q, k, v, log_decay, seq_start=None, h0=None, scale=1.0, want
     """Runs ssm_linattn_forward; returns (y, hT), hT None unless want_state or
     given.  y has v's shape; hT may be h0.  With seq_start, rows of y outside
     the sequences are not written."""
-    dims, device, lead, ins = _setup(q, k, v, log_decay, scale, seq_start)
+    device = _gpu(q, "q")
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return linattn_forward(q, k, v, log_decay, seq_start, h0, scale, want_state, y, hT, ws)
+    dims, lead, hv, ins = _setup(q, k, v, log_decay, scale, seq_start, device)
     states = (dims.S, dims.Hv, dims.dk, dims.dv)
     ins.h0 = _dense(h0, "h0", states, device, torch.float32)
-    with _context(device, stream) as handle:
-        if y is None:
-            y = torch.empty(v.shape, dtype=v.dtype, device=device)
-        _, _, ldy = _rows(y, "y", lead, device, q.dtype, dims.Hv, dims.dv)
-        if hT is None and want_state:
-            hT = torch.empty(states, dtype=torch.float32, device=device)
-        end = _dense(hT, "hT", states, device, torch.float32)
-        w = _workspace(ws, linattn_workspace_bytes(dims), device)
-        _check(lib.ssm_linattn_forward(ctypes.byref(dims), ctypes.byref(ins), y.data_ptr(), ldy, end,
-                                       None if w is None else w.data_ptr(), 0 if w is None else w.numel(), handle),
-               "ssm_linattn_forward")
+    if y is None:
+        y = torch.empty_like(v, memory_format=torch.contiguous_format)
+        ldy = hv[0] * hv[1]
+    else:
+        _, ldy = _rows(y, "y", lead, device, q.dtype, hv)
+    if hT is None and want_state:
+        hT = torch.empty(states, dtype=torch.float32, device=q.device)
+    end = _dense(hT, "hT", states, device, torch.float32)
+    w, n = _ws_args(_workspace(ws, linattn_workspace_bytes(dims), device))
+    _check(lib.ssm_linattn_forward(ctypes.byref(dims), ctypes.byref(ins), y.data_ptr(), ldy, end, w, n,
+                                   _raw_stream(device)), "ssm_linattn_forward")
     return y, hT
 
 
@@ -197,28 +205,27 @@ def linattn_grad(q, k, v, log_decay, dy, seq_start=None, h0=None, dhT=None, scal
     """Runs ssm_linattn_grad; returns the gradient dict.  want: names among
     GRADS (default: all, dh0 only with an h0).  grads: output tensors by
     name (then they alone are computed)."""
-    dims, device, lead, ins = _setup(q, k, v, log_decay, scale, seq_start)
+    device = _gpu(q, "q")
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return linattn_grad(q, k, v, log_decay, dy, seq_start, h0, dhT, scale, want, grads, ws)
+    dims, lead, hv, ins = _setup(q, k, v, log_decay, scale, seq_start, device)
     states = (dims.S, dims.Hv, dims.dk, dims.dv)
     ins.h0 = _dense(h0, "h0", states, device, torch.float32)
     end = _dense(dhT, "dhT", states, device, torch.float32)
-    _, _, lddy = _rows(dy, "dy", lead, device, q.dtype, dims.Hv, dims.dv)
+    _, lddy = _rows(dy, "dy", lead, device, q.dtype, hv)
     like = {"dq": (q.shape, q.dtype), "dk": (k.shape, q.dtype), "dv": (v.shape, q.dtype),
             "dlog_decay": (log_decay.shape, torch.float32), "dh0": (states, torch.float32)}
-    with _context(device, stream) as handle:
-        if grads is None:
-            names = want if want is not None else GRADS if h0 is not None else GRADS[:4]
-            for n in names:
-                if n not in like:
-                    _bad(f"want: {n!r} is none of {GRADS}")
-            grads = {n: torch.empty(like[n][0], dtype=like[n][1], device=device) for n in names}
-        for n in grads:
-            if n not in like:
-                _bad(f"grads: {n!r} is none of {GRADS}")
-        g = LinattnGrads(*(_dense(grads.get(n), n, like[n][0], device, like[n][1]) for n in GRADS))
-        w = _workspace(ws, linattn_workspace_bytes(dims, g), device)
-        _check(lib.ssm_linattn_grad(ctypes.byref(dims), ctypes.byref(ins), dy.data_ptr(), lddy, end, ctypes.byref(g),
-                                    None if w is None else w.data_ptr(), 0 if w is None else w.numel(), handle),
-               "ssm_linattn_grad")
+    names = grads if grads is not None else want if want is not None else GRADS if h0 is not None else GRADS[:4]
+    for name in names:
+        if name not in like:
+            _bad(f"gradient {name!r} is none of {GRADS}")
+    if grads is None:
+        grads = {name: torch.empty(like[name][0], dtype=like[name][1], device=q.device) for name in names}
+    g = LinattnGrads(*(_dense(grads.get(name), name, like[name][0], device, like[name][1]) for name in GRADS))
+    w, n = _ws_args(_workspace(ws, linattn_workspace_bytes(dims, g), device))
+    _check(lib.ssm_linattn_grad(ctypes.byref(dims), ctypes.byref(ins), dy.data_ptr(), lddy, end, ctypes.byref(g), w, n,
+                                _raw_stream(device)), "ssm_linattn_grad")
     return grads
 
 
@@ -226,14 +233,19 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
     """Runs ssm_linattn_step: row t of q, k [B, Hk, dk] and v [B, Hv, dv] is
     the next token of the sequence with state[t] ([B, Hv, dk, dv], updated in
     place).  Returns y [B, Hv, dv]."""
-    dims, device, lead, ins = _setup(q, k, v, log_decay, scale, None, step=True)
+    device = _gpu(q, "q")
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return linattn_step(q, k, v, log_decay, state, scale, y)
+    dims, lead, hv, ins = _setup(q, k, v, log_decay, scale, None, device, step=True)
     if state is None:
         _bad("state is required")
     st = _dense(state, "state", (dims.T, dims.Hv, dims.dk, dims.dv), device, torch.float32)
-    with _context(device, stream) as handle:
-        if y is None:
-            y = torch.empty(v.shape, dtype=v.dtype, device=device)
-        _, _, ldy = _rows(y, "y", lead, device, q.dtype, dims.Hv, dims.dv)
-        _check(lib.ssm_linattn_step(ctypes.byref(dims), ctypes.byref(ins), st, y.data_ptr(), ldy, handle),
-               "ssm_linattn_step")
+    if y is None:
+        y = torch.empty_like(v, memory_format=torch.contiguous_format)
+        ldy = hv[0] * hv[1]
+    else:
+        _, ldy = _rows(y, "y", lead, device, q.dtype, hv)
+    _check(lib.ssm_linattn_step(ctypes.byref(dims), ctypes.byref(ins), st, y.data_ptr(), ldy, _raw_stream(device)),
+           "ssm_linattn_step")
     return y

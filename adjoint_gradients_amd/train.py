@@ -7,7 +7,7 @@ import torch
 
 from . import SsmError, alloc_workspace, lib
 from . import _check
-from .linattn import _IO, _bad, _context, _dense, _gpu, _workspace
+from .linattn import _IO, _bad, _current_device, _dense, _gpu, _on, _raw_stream, _workspace
 
 _VP, _I64 = ctypes.c_void_p, ctypes.c_int64
 lib.ssm_add_norm.argtypes = [_I64, _I64, ctypes.c_int32, _VP, _VP, _VP, ctypes.c_float, _VP, _VP, _VP, _VP]
@@ -25,12 +25,12 @@ lib.ssm_clip_grads.restype = ctypes.c_int
 _F32 = torch.float32
 
 
-def _shape2(t, name: str):
-    _gpu(t, name, None, _F32)
-    if t.dim() < 2 or t.numel() == 0:
-        _bad(f"{name}: expected rows of channels, got shape {tuple(t.shape)}")
-    P = t.shape[-1]
-    return t.numel() // P, P
+def _sizes(t, name: str):
+    """Rows and channels of a float32 tensor [..., P]."""
+    shape = t.shape
+    if len(shape) < 2 or t.numel() == 0:
+        _bad(f"{name}: expected rows of channels, got shape {tuple(shape)}")
+    return t.numel() // shape[-1], shape[-1]
 
 
 def add_norm(r, y, norm_scale, eps=1e-5, r_out=None, x=None, rinv=None, io=None, stream=None):
@@ -38,32 +38,34 @@ def add_norm(r, y, norm_scale, eps=1e-5, r_out=None, x=None, rinv=None, io=None,
     rinv).  r [..., P] float32; y of the same shape in the io dtype, or None
     (then r_out is r itself unless given, and io, "f32" or "bf16", names x's
     dtype).  r_out may be r.  rinv [...] float32 is 1 / rms, for the gradient."""
-    T, P = _shape2(r, "r")
-    device, shape = r.device, r.shape
-    if y is not None:
-        _gpu(y, "y")
-        dt = y.dtype
-    elif x is not None:
-        _gpu(x, "x")
-        dt = x.dtype
+    device = _gpu(r, "r", None, _F32)
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return add_norm(r, y, norm_scale, eps, r_out, x, rinv, io)
+    T, P = _sizes(r, "r")
+    shape = r.shape
+    like = y if y is not None else x
+    if like is not None:
+        _gpu(like, "y" if y is not None else "x", device)
+        dt = like.dtype
     else:
         dt = {"f32": _F32, "bf16": torch.bfloat16}.get(io)
     if dt not in _IO:
         _bad("the io dtype is bfloat16 or float32")
+    if norm_scale is None:
+        _bad("norm_scale is required")
     rp = _dense(r, "r", shape, device, _F32)
     yp = _dense(y, "y", shape, device, dt)
-    _gpu(norm_scale, "norm_scale", device, _F32)
     gp = _dense(norm_scale, "norm_scale", (P,), device, _F32)
-    with _context(device, stream) as handle:
-        if r_out is None:
-            r_out = r if y is None else torch.empty(shape, dtype=_F32, device=device)
-        if x is None:
-            x = torch.empty(shape, dtype=dt, device=device)
-        if rinv is None:
-            rinv = torch.empty(shape[:-1], dtype=_F32, device=device)
-        _check(lib.ssm_add_norm(T, P, _IO[dt], rp, yp, gp, float(eps), _dense(r_out, "r_out", shape, device, _F32),
-                                _dense(x, "x", shape, device, dt), _dense(rinv, "rinv", shape[:-1], device, _F32),
-                                handle), "ssm_add_norm")
+    if r_out is None:
+        r_out = r if y is None else torch.empty_like(r)
+    if x is None:
+        x = torch.empty_like(r, dtype=dt)
+    if rinv is None:
+        rinv = torch.empty(shape[:-1], dtype=_F32, device=r.device)
+    _check(lib.ssm_add_norm(T, P, _IO[dt], rp, yp, gp, eps, _dense(r_out, "r_out", shape, device, _F32),
+                            _dense(x, "x", shape, device, dt), _dense(rinv, "rinv", shape[:-1], device, _F32),
+                            _raw_stream(device)), "ssm_add_norm")
     return x, r_out, rinv
 
 
@@ -71,29 +73,33 @@ def add_norm_grad(r_out, rinv, norm_scale, dx, dr_out=None, dr=None, want_scale=
     """Gradient of add_norm; returns (dr, dnorm_scale).  dr (float32) is the
     cotangent of r and of y: dr_out, the cotangent of r_out from elsewhere
     (None: zero), plus the norm's part.  dr may be dr_out."""
-    T, P = _shape2(r_out, "r_out")
-    device, shape = r_out.device, r_out.shape
+    device = _gpu(r_out, "r_out", None, _F32)
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return add_norm_grad(r_out, rinv, norm_scale, dx, dr_out, dr, want_scale, ws)
+    T, P = _sizes(r_out, "r_out")
+    shape = r_out.shape
     _gpu(dx, "dx", device)
-    if dx.dtype not in _IO:
-        _bad(f"dx: dtype {dx.dtype}, expected bfloat16 or float32")
+    dt = dx.dtype
+    if dt not in _IO:
+        _bad(f"dx: dtype {dt}, expected bfloat16 or float32")
     if rinv is None or norm_scale is None:
         _bad("rinv and norm_scale are required")
     rp = _dense(r_out, "r_out", shape, device, _F32)
     ip = _dense(rinv, "rinv", shape[:-1], device, _F32)
     gp = _dense(norm_scale, "norm_scale", (P,), device, _F32)
-    xp = _dense(dx, "dx", shape, device, dx.dtype)
+    xp = _dense(dx, "dx", shape, device, dt)
     cp = _dense(dr_out, "dr_out", shape, device, _F32)
     nbytes = lib.ssm_add_norm_grad_workspace_bytes(T, P)
     if nbytes == 0:
         raise SsmError(4, "ssm_add_norm_grad_workspace_bytes")
-    with _context(device, stream) as handle:
-        if dr is None:
-            dr = torch.empty(shape, dtype=_F32, device=device)
-        dscale = torch.empty(P, dtype=_F32, device=device) if want_scale else None
-        w = _workspace(ws, nbytes, device)
-        _check(lib.ssm_add_norm_grad(T, P, _IO[dx.dtype], rp, ip, gp, xp, cp, _dense(dr, "dr", shape, device, _F32),
-                                     None if dscale is None else dscale.data_ptr(), w.data_ptr(), w.numel(), handle),
-               "ssm_add_norm_grad")
+    if dr is None:
+        dr = torch.empty_like(r_out)
+    dscale = torch.empty_like(norm_scale) if want_scale else None
+    w = _workspace(ws, nbytes, device)
+    _check(lib.ssm_add_norm_grad(T, P, _IO[dt], rp, ip, gp, xp, cp, _dense(dr, "dr", shape, device, _F32),
+                                 None if dscale is None else dscale.data_ptr(), w.data_ptr(), w.numel(),
+                                 _raw_stream(device)), "ssm_add_norm_grad")
     return dr, dscale
 
 
@@ -112,33 +118,38 @@ def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
             ts.append(g)
     if not ts:
         _bad("clip_grads: no gradients")
-    _gpu(ts[0], "grads[0]")
-    device, dt = ts[0].device, ts[0].dtype
+    device = _gpu(ts[0], "grads[0]")
+    if stream is not None or device != _current_device():
+        with _on(device, stream):
+            return clip_grads(ts, max_norm, out, norm, ws)
+    dt = ts[0].dtype
     if dt not in _IO:
         _bad(f"grads: dtype {dt}, expected bfloat16 or float32")
     if not max_norm > 0:
         _bad("max_norm must be positive")
-    os_ = ts if out is None else list(out)
-    if len(os_) != len(ts):
-        _bad(f"clip_grads: {len(os_)} outputs for {len(ts)} gradients")
     n = len(ts)
-    ins = (_VP * n)(*(_dense(t, f"grads[{i}]", t.shape, device, dt) for i, t in enumerate(ts)))
+    pi = [_dense(t, "a gradient", t.shape, device, dt) for t in ts]
     if out is None:
-        outs = ins
-        seen = set(t.data_ptr() for t in ts if t.numel())
-        if len(seen) != sum(1 for t in ts if t.numel()):
+        po = pi
+        if len(set(pi)) != n and len({p for p, t in zip(pi, ts) if t.numel()}) != sum(1 for t in ts if t.numel()):
             _bad("clip_grads: a gradient is given twice")
     else:
-        outs = (_VP * n)(*(_dense(o, f"out[{i}]", ts[i].shape, device, dt) for i, o in enumerate(os_)))
-    ns = (_I64 * n)(*(t.numel() for t in ts))
+        out = list(out)
+        if len(out) != n:
+            _bad(f"clip_grads: {len(out)} outputs for {n} gradients")
+        po = [_dense(o, "an output", t.shape, device, dt) for o, t in zip(out, ts)]
+        if None in po:
+            _bad("clip_grads: an output is missing")
+    ptrs, counts = _VP * n, _I64 * n
+    ns = counts(*[t.numel() for t in ts])
     nbytes = lib.ssm_clip_grads_workspace_bytes(n, ns)
     if nbytes == 0:
         raise SsmError(4, "ssm_clip_grads_workspace_bytes")
-    with _context(device, stream) as handle:
-        if norm is None:
-            norm = torch.empty(1, dtype=_F32, device=device)
-        w = _workspace(ws, nbytes, device)
-        _check(lib.ssm_clip_grads(n, ins, outs if max_norm != float("inf") or out is not None else None, ns, _IO[dt],
-                                  float(max_norm), _dense(norm, "norm", (1,), device, _F32), w.data_ptr(), w.numel(),
-                                  handle), "ssm_clip_grads")
+    if norm is None:
+        norm = torch.empty(1, dtype=_F32, device=ts[0].device)
+    w = _workspace(ws, nbytes, device)
+    measure = out is None and max_norm == float("inf")
+    _check(lib.ssm_clip_grads(n, ptrs(*pi), None if measure else ptrs(*po), ns, _IO[dt], max_norm,
+                              _dense(norm, "norm", (1,), device, _F32), w.data_ptr(), w.numel(), _raw_stream(device)),
+           "ssm_clip_grads")
     return norm
