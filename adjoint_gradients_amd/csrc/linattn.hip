@@ -12,7 +12,7 @@
 
 #include "../../include/ssm_linattn.h"
 #include "abi_util.hpp"
-#include "linattn.hpp"
+#include "linattn_seqs.hpp"
 #include "ssm_common.hpp"
 
 namespace la {
@@ -112,6 +112,92 @@ __global__ __launch_bounds__(256) void k_la_group_sum(Seqs sq, int32_t Hk, int32
     }
     T* o = out + th * d + c;
     ssm::store_io(o, s.x); ssm::store_io(o + 1, s.y); ssm::store_io(o + 2, s.z); ssm::store_io(o + 3, s.w);
+  }
+}
+
+// The decay gradient from the runs' terms, one workgroup per segment and
+// head: for the chunks of each anchor, from the last,
+//   dg_t = (sum over i >= t, forward run) + (sum over j < t, reverse run) + x_c,
+// x_c = e^{G_L} <S, D> at the anchor; then x of the chunk before is x_c plus
+// c's sum over all i less its own sum over all j.
+struct DecayArgs {
+  Seqs sq;
+  int32_t Hv, ch, n4;           // tokens of a chunk; float4s of a padded state
+  const float* log_decay;
+  int64_t ld_decay;
+  const float *tok_f, *tok_r;   // [Hv][T]
+  const float *anchor_s, *anchor_d;
+  float* dg_tok;                // [T][Hv] or null
+  double* dg_seg;               // [slots][Hv] or null
+};
+
+__device__ __forceinline__ double wg_sum(double v, double* red) {
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__global__ __launch_bounds__(256) void k_la_decay_grad(DecayArgs a) {
+  __shared__ double red[4], xs[kAnchor], all_i[kAnchor], all_j[kAnchor];
+  const uint32_t slot = blockIdx.x;
+  const int h = blockIdx.y;
+  Segment sg;
+  const bool have = find_segment(a.sq, slot, a.ch, &sg);
+  double sum = 0.0;
+  if (have) {
+    const int nch = (sg.t1 - sg.t0 + a.ch - 1) / a.ch;
+    const float* const tf = a.tok_f + static_cast<int64_t>(h) * a.sq.T;
+    const float* const tr = a.tok_r + static_cast<int64_t>(h) * a.sq.T;
+    for (int k0 = 0; k0 < nch; k0 += kAnchor) {
+      const int c = nch - 1 - k0;  // the anchor
+      const int nc = c + 1 < kAnchor ? c + 1 : kAnchor;
+      const int64_t o = ((anchor_slot(sg, slot) + k0 / kAnchor) * a.Hv + h) * a.n4;
+      const float4* const ps = reinterpret_cast<const float4*>(a.anchor_s) + o;
+      const float4* const pd = reinterpret_cast<const float4*>(a.anchor_d) + o;
+      double dot = 0.0;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < a.n4; i += 256) {
+        const float4 s = ps[i], d = pd[i];
+        dot += static_cast<double>(fmaf(s.x, d.x, s.y * d.y) + fmaf(s.z, d.z, s.w * d.w));
+      }
+      const int t = sg.t0 + c * a.ch + static_cast<int>(threadIdx.x);
+      double lg = 0.0;
+      if (static_cast<int>(threadIdx.x) < a.ch && t < sg.t1)
+        lg = decay_log2(a.log_decay[t * a.ld_decay + h]);
+      lg = wg_sum(lg, red);
+      dot = wg_sum(dot, red);
+      // sums of chunk c - i over all its tokens, for the boundary on either side
+      if (static_cast<int>(threadIdx.x) < nc) {
+        const int first = sg.t0 + (c - static_cast<int>(threadIdx.x)) * a.ch;
+        const int end = first + a.ch < sg.t1 ? first + a.ch : sg.t1;
+        all_i[threadIdx.x] = static_cast<double>(tf[first]);
+        all_j[threadIdx.x] = static_cast<double>(tr[end - 1]);
+      }
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < nc) {
+        double x = static_cast<double>(exp2_split(lg)) * dot;
+        for (int i = 0; i < static_cast<int>(threadIdx.x); i++) x += all_i[i] - all_j[i + 1];
+        xs[threadIdx.x] = x;
+      }
+      __syncthreads();
+      const int t0 = sg.t0 + (c + 1 - nc) * a.ch;
+      const int t1 = sg.t0 + (c + 1) * a.ch < sg.t1 ? sg.t0 + (c + 1) * a.ch : sg.t1;
+      for (int u = t0 + static_cast<int>(threadIdx.x); u < t1; u += 256) {
+        const int j = (u - sg.t0) / a.ch;
+        const double before = u == sg.t0 + j * a.ch ? 0.0 : static_cast<double>(tr[u - 1]);
+        const double dg = static_cast<double>(tf[u]) + before + xs[c - j];
+        if (a.dg_tok) a.dg_tok[static_cast<int64_t>(u) * a.Hv + h] = static_cast<float>(dg);
+        sum += dg;
+      }
+      __syncthreads();
+    }
+  }
+  if (a.dg_seg) {
+    sum = wg_sum(sum, red);
+    if (threadIdx.x == 0) a.dg_seg[static_cast<int64_t>(slot) * a.Hv + h] = sum;
   }
 }
 
@@ -267,8 +353,8 @@ int64_t segment_tokens(const ssm_linattn_dims* d, bool packed, int runs) {
 struct Ws {
   float* seg[2];        // segment states: forward, adjoint
   float* seg_decay[2];
-  float* tok;
-  float* chunk_states;
+  float* tok[2];        // the decay gradient's terms: forward run, reverse run
+  float* anchors[2];
   double* dg_seg;
   float* part[2];       // dq, dk per value head
 };
@@ -288,7 +374,7 @@ Plan make_plan(const ssm_linattn_dims* d, const ssm_linattn_grads* g, bool packe
   p.need_s = !g || g->dq || g->dlog_decay;
   p.need_d = g && (g->dk || g->dv || g->dlog_decay || g->dh0);
   p.dg = g && g->dlog_decay;
-  p.L = segment_tokens(d, packed, g ? 2 : 1);
+  p.L = segment_tokens(d, packed, g ? 3 : 1);
   p.slots = slot_count(d->T, d->S, p.L);
   p.split = p.L < longest(d, packed);
   return p;
@@ -306,9 +392,12 @@ Ws carve(abi::Carver& cv, const ssm_linattn_dims* d, const ssm_linattn_grads* g,
       }
   }
   if (p.dg) {
-    w.tok = cv.take<float>(static_cast<size_t>(d->T) * d->Hv);
-    const int64_t cs = slot_count(d->T, d->S, chunk_tokens(d->io == SSM_BF16));
-    w.chunk_states = cv.take<float>(static_cast<size_t>(cs) * d->Hv * state_floats(d->dk, d->dv));
+    // chunk slots of consecutive segments are kAnchor apart at least where their anchors are
+    const int64_t n = slot_count(d->T, d->S, chunk_tokens(d->io == SSM_BF16)) / kAnchor + p.slots + 1;
+    for (int i = 0; i < 2; i++) {
+      w.tok[i] = cv.take<float>(static_cast<size_t>(d->T) * d->Hv);
+      w.anchors[i] = cv.take<float>(static_cast<size_t>(n) * d->Hv * state_floats(d->dk, d->dv));
+    }
     if (!d->decay_tokens) w.dg_seg = cv.take<double>(hs);
   }
   if (g && d->Hk != d->Hv) {
@@ -331,11 +420,16 @@ size_t plan_bytes(const ssm_linattn_dims* d, const ssm_linattn_grads* g) {
 
 bool any_grad(const ssm_linattn_grads* g) { return g->dq || g->dk || g->dv || g->dlog_decay || g->dh0; }
 
-hipError_t launch(Kernel k, const ssm_linattn_dims* d, const Args& a, int nz, hipStream_t st) {
+hipError_t launch(Kernel k, const ssm_linattn_dims* d, Args& a, int nz, hipStream_t st) {
+  // Heads that share q and k stay on one XCD where that still leaves each of
+  // the 8 XCDs several units of work.
+  const int64_t slots = slot_count(d->T, d->S, a.sq.L);
+  a.nz = nz;
+  a.unit_heads = slots * d->Hk >= 64 ? d->Hv / d->Hk : 1;
+  a.units = static_cast<uint32_t>(slots * (d->Hv / a.unit_heads));
   const bool wide = padded(d->dk) == 128;
-  if (d->io == SSM_BF16)
-    return wide ? launch_bf16_128(k, d->dv, a, nz, st) : launch_bf16_64(k, d->dv, a, nz, st);
-  return wide ? launch_f32_128(k, d->dv, a, nz, st) : launch_f32_64(k, d->dv, a, nz, st);
+  if (d->io == SSM_BF16) return wide ? launch_bf16_128(k, d->dv, a, st) : launch_bf16_64(k, d->dv, a, st);
+  return wide ? launch_f32_128(k, d->dv, a, st) : launch_f32_64(k, d->dv, a, st);
 }
 
 Args base_args(const ssm_linattn_dims* d, const ssm_linattn_in* in, const Plan& p) {
@@ -454,8 +548,8 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   rq.sm = 1; rq.sn = d->dv;
   rq.out = w.part[0] ? static_cast<void*>(w.part[0]) : g->dq;
   rq.ldo = part_ld;
-  rq.tok = w.tok;
-  rq.chunk_states = w.chunk_states;
+  rq.tok = w.tok[0];
+  rq.anchors = w.anchors[0];
   // dv: the state's adjoint D, entered by dhT
   Run rv = make_run(k, q, o, 1.0f, d->scale);
   rv.s0 = dhT;
@@ -471,29 +565,26 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   rk.sm = 1; rk.sn = d->dv;
   rk.out = w.part[1] ? static_cast<void*>(w.part[1]) : g->dk;
   rk.ldo = part_ld;
-  rk.tok = w.tok;
-  rk.chunk_states = w.chunk_states;
-  rk.dg_tok = d->decay_tokens ? g->dlog_decay : nullptr;
-  rk.dg_seg = w.dg_seg;
+  rk.tok = w.tok[1];
+  rk.anchors = w.anchors[1];
   const bool need_k = g->dk || p.dg;
   if (need_k) rk.s_end = g->dh0;
   else rv.s_end = g->dh0;
   const bool need_v = g->dv || (!need_k && g->dh0);
+  a.run[0] = g->dq || p.dg ? rq : Run{};
+  a.run[1] = need_k ? rk : Run{};
+  a.run[2] = need_v ? rv : Run{};
+  if ((e = launch(p.dg ? kGradDecay : kGradPlain, d, a, need_v ? 3 : 2, st)) != hipSuccess) return e;
   if (p.dg) {
-    a.run[0] = rq;
-    a.run[1] = rv;
-    if ((e = launch(kGradFirst, d, a, need_v ? 2 : 1, st)) != hipSuccess) return e;
-    a.run[0] = rk;
-    if ((e = launch(kGradSecond, d, a, 1, st)) != hipSuccess) return e;
+    const DecayArgs da{a.sq, d->Hv, chunk_tokens(d->io == SSM_BF16),
+                       static_cast<int32_t>(state_floats(d->dk, d->dv) / 4), in->log_decay, a.ld_decay, w.tok[0],
+                       w.tok[1], w.anchors[0], w.anchors[1], d->decay_tokens ? g->dlog_decay : nullptr, w.dg_seg};
+    k_la_decay_grad<<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(d->Hv)), 256, 0, st>>>(da);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     if (!d->decay_tokens) {
       k_la_decay_sum<<<static_cast<unsigned>(d->Hv), 256, 0, st>>>(p.slots, d->Hv, w.dg_seg, g->dlog_decay);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-  } else {
-    a.run[0] = g->dq ? rq : Run{};
-    a.run[1] = need_v ? rv : Run{};
-    a.run[2] = need_k ? rk : Run{};
-    if ((e = launch(kGradPlain, d, a, 3, st)) != hipSuccess) return e;
   }
   if (w.part[0] && (e = group_sum(d, a.sq, w.part[0], g->dq, st)) != hipSuccess) return e;
   if (w.part[1] && (e = group_sum(d, a.sq, w.part[1], g->dk, st)) != hipSuccess) return e;

@@ -37,10 +37,8 @@ struct Run {
   float* s_end;                    // [S][Hv] the state leaving the sequences, or null
   int32_t sm, sn;                  // strides of a state's dm and dn index
   void* out;                       // token rows of Hv heads, or null
-  float* tok;                      // [T][Hv] decay-gradient terms (written by the forward run, read by the reverse)
-  float* chunk_states;             // [chunk slots][Hv][dm][dn] (padded) states entering each chunk
-  float* dg_tok;                   // [T][Hv] decay gradient, or null
-  double* dg_seg;                  // [slots][Hv] its sums over segments, or null
+  float* tok;                      // [Hv][T] sums inside the chunk of the decay gradient's terms
+  float* anchors;                  // [anchor slots][Hv][dm][dn] (padded) states kept for it
 };
 
 struct Args {
@@ -49,16 +47,20 @@ struct Args {
   const float* log_decay;
   int64_t ld_decay;                // Hv, or 0 for one decay per head
   int32_t sum_heads;               // dq and dk are float32, one per value head
+  int32_t nz;                      // runs of the launch
+  int32_t unit_heads;              // consecutive heads whose workgroups stay on one XCD
+  uint32_t units;                  // segment slots x Hv / unit_heads
   Run run[3];
 };
 
 enum Kernel {
   kForward,    // run 0: y
-  kAggregate,  // run 0: the segments' state sums, forward in time; run 1 (if any): in reverse
-  kGradFirst,  // run 0: dq and the decay gradient's forward terms; run 1: dv
-  kGradSecond, // run 0: dk and the decay gradient
-  kGradPlain   // runs 0, 1, 2: dq, dv, dk without the decay gradient
+  kAggregate,  // run 0: the segments' state sums, forward in time; run 1: in reverse
+  kGradPlain,  // runs 0, 1, 2: dq, dk, dv (a run without operands is left out)
+  kGradDecay   // the same with the decay gradient's terms
 };
+
+constexpr int kAnchor = 8;  // chunks between kept states
 
 // Tokens of a chunk: 64 for bf16, 32 for fp32 (the same LDS bytes a tile).
 constexpr int chunk_tokens(bool bf16) { return bf16 ? 64 : 32; }
@@ -69,10 +71,10 @@ inline int padded(int d) { return d <= 64 ? 64 : 128; }
 // Floats of one padded state.
 inline int64_t state_floats(int dk, int dv) { return static_cast<int64_t>(padded(dk)) * padded(dv); }
 
-// One launch over every segment slot, head and run; by io type and padded dk.
-hipError_t launch_bf16_64(Kernel k, int dv, const Args& a, int nz, hipStream_t st);
-hipError_t launch_bf16_128(Kernel k, int dv, const Args& a, int nz, hipStream_t st);
-hipError_t launch_f32_64(Kernel k, int dv, const Args& a, int nz, hipStream_t st);
-hipError_t launch_f32_128(Kernel k, int dv, const Args& a, int nz, hipStream_t st);
+// One launch over every segment slot, head and run, by io type and padded dk.
+hipError_t launch_bf16_64(Kernel k, int dv, const Args& a, hipStream_t st);
+hipError_t launch_bf16_128(Kernel k, int dv, const Args& a, hipStream_t st);
+hipError_t launch_f32_64(Kernel k, int dv, const Args& a, hipStream_t st);
+hipError_t launch_f32_128(Kernel k, int dv, const Args& a, hipStream_t st);
 
 }  // namespace la

@@ -19,8 +19,10 @@
 //   dg_t = sum_{j < t <= i} M_ij + sum_{i >= t} R_i + sum_{j < t} K_j + e^{G_L} <S, D>.
 // Nothing in it cancels; the shorter identity, the suffix sum over the whole
 // sequence of <q, dq> - <k, dk>, loses three digits over 65536 tokens.  The
-// forward run stores the states entering each chunk so that the reverse run
-// can form <S, D>.
+// term e^{G_L} <S, D> is formed where both runs keep their state, at every
+// kAnchor-th chunk, and carried to the chunks between: across a boundary
+// e^{G_L} <S, D> of the later chunk + its sum of R = that of the earlier one
+// + its sum of K.  (Kept at every chunk, the states were 40% of the traffic.)
 //
 // One workgroup of four wavefronts walks the chunks of one segment of one
 // sequence for one head.  The state stays in the accumulators of v_mfma
@@ -33,11 +35,11 @@
 // Rounding: products are bf16 x bf16 summed in fp32 (or fp32 throughout).
 // The decayed scores are rounded to bf16 before they multiply V, and the
 // state to bf16 where it multiplies Q: both errors are of the size of the
-// output's own rounding.  What ends in an fp32 output (states, decay
-// gradient) is split into bf16 parts that together hold the fp32 value to
-// 2^-17: the weighted V of the state's update, and the state in the runs
-// that form the decay gradient.
-#include "linattn.hpp"
+// output's own rounding.  Where a product ends in an fp32 output (states,
+// decay gradient), its fp32 operand is split into bf16 parts that together
+// hold it whole: the weighted V of the state's update, and the state in the
+// runs that form the decay gradient.
+#include "linattn_seqs.hpp"
 #include "ssm_common.hpp"
 
 namespace la {
@@ -51,13 +53,16 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
 constexpr int kThreads = 256;  // four wavefronts
-constexpr float kLn2 = 0.69314718055994531f;
 
 // Modes of a run.
 constexpr int kOut = 0;       // out
 constexpr int kAgg = 1;       // only the state's sum over the segment
-constexpr int kOutFwdDg = 2;  // out, the decay gradient's forward terms, the chunk states
-constexpr int kOutRevDg = 3;  // out and the decay gradient
+constexpr int kOutFwdDg = 2;  // out, the decay gradient's terms of the pairs that end here, the anchor states
+constexpr int kOutRevDg = 3;  // out, the terms of the pairs that start here, the anchor states' adjoints
+
+// bf16 parts of an fp32 operand whose product ends in an fp32 output: three
+// hold all 24 bits.
+constexpr int kParts = 3;
 
 template <class T>
 struct Cfg {
@@ -83,7 +88,7 @@ struct Lds {
   static constexpr int wk = 3 * C::CH;
   static constexpr int wc = wk + 2 * C::CH;
   static constexpr int red = wc + 4;
-  static constexpr int floats = red + (MODE >= kOutFwdDg ? (4 + C::JW + C::NIB) * C::CH + 4 : 0);
+  static constexpr int floats = red + (MODE >= kOutFwdDg ? (4 + C::JW + C::NIB) * C::CH : 0);
   static constexpr int bytes = f + floats * 4;
 };
 
@@ -104,58 +109,10 @@ __device__ __forceinline__ int at_p(int i, int j) {
   return i * Cfg<T>::CH + ((j / EPV) ^ ((i >> 1) & 7)) * EPV + j % EPV;
 }
 
-struct Segment {
-  int32_t seq;
-  int32_t t0, t1;      // its tokens
-  int32_t chunk_slot;  // of its first chunk
-  bool first, last;    // of its sequence
-};
-
-// The segment of a slot; false if the slot has none.  The sequence is found
-// by bisection over the first slots start[s] / L + s, which increase with s.
-__device__ __forceinline__ bool find_segment(const Seqs& sq, uint32_t slot, int ch, Segment* o) {
-  const uint32_t L = static_cast<uint32_t>(sq.L), T = static_cast<uint32_t>(sq.T);
-  const uint32_t n = T / static_cast<uint32_t>(sq.S);
-  auto start = [&](int32_t s) -> uint32_t {
-    if (!sq.start) return n * static_cast<uint32_t>(s);
-    const int32_t v = sq.start[s];
-    return v < 0 ? 0u : static_cast<uint32_t>(v) > T ? T : static_cast<uint32_t>(v);
-  };
-  int32_t lo = 0, hi = sq.S - 1;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) / 2;
-    if (start(mid) / L + static_cast<uint32_t>(mid) <= slot) lo = mid;
-    else hi = mid - 1;
-  }
-  const uint32_t a = start(lo);
-  uint32_t b = start(lo + 1);
-  b = b < a ? a : b;
-  const uint32_t base = a / L + static_cast<uint32_t>(lo);
-  if (slot < base) return false;
-  const uint32_t j = slot - base;
-  const uint32_t nseg = (b - a + L - 1) / L;
-  if (j >= (nseg ? nseg : 1u)) return false;
-  o->seq = lo;
-  o->t0 = static_cast<int32_t>(a + j * L);
-  o->t1 = static_cast<int32_t>(b - a - j * L < L ? b : a + (j + 1) * L);
-  o->chunk_slot = static_cast<int32_t>(a / static_cast<uint32_t>(ch)) + lo + static_cast<int32_t>(j * (L / ch));
-  o->first = j == 0;
-  o->last = j + 1 >= nseg;
-  return true;
-}
-
 // Barrier that orders LDS accesses only.  The fence of __syncthreads() also
 // waits for every global access in flight, which here are the next chunk's
 // loads and the previous one's stores.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
-// 2^x of a 64-bit x, to fp32 accuracy also for large |x|.
-__device__ __forceinline__ float exp2_split(double x) {
-  const float h = static_cast<float>(x);
-  const float l = static_cast<float>(x - static_cast<double>(h));
-  const float e = ssm::fast_exp2(h);
-  return fmaf(e, l * kLn2, e);
-}
 
 // A 64-bit value moved across lanes by a DPP control; lanes without a source
 // (or outside the row mask) get 0.
@@ -180,12 +137,21 @@ __device__ __forceinline__ double prefix_sum(double v) {
   return v;
 }
 
-template <int D>
-__device__ __forceinline__ float xor_add(float v) { return v + __shfl_xor(v, D, 64); }
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(
+                 float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
 
-// Sums over the 16 lanes of a group, and over the four groups.
-__device__ __forceinline__ float sum16(float v) { return xor_add<8>(xor_add<4>(xor_add<2>(xor_add<1>(v)))); }
-__device__ __forceinline__ float sum_groups(float v) { return xor_add<32>(xor_add<16>(v)); }
+// Sums over the 16 lanes of a group (rotations by 8, 4, 2, 1), and over the
+// four groups (swaps of rows and of halves); every lane gets the sum.
+__device__ __forceinline__ float sum16(float v) {
+  return dpp_add<0x121>(dpp_add<0x122>(dpp_add<0x124>(dpp_add<0x128>(v))));
+}
+__device__ __forceinline__ float sum_groups(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return ssm::xor_sum<32>(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
 
 __device__ __forceinline__ f32x4_t mfma_bf16(bf16x8_t a, bf16x8_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -227,12 +193,12 @@ __device__ __forceinline__ bf16x8_t read_tr(bf16_t* tile, int t0, int c0, int l1
   return __builtin_bit_cast(bf16x8_t, p);
 }
 
-// Rows of d elements, ld apart, from a chunk's first token on; accesses past
-// row nv read zero and store nothing (offsets are range-checked in hardware,
-// so no lane mask or branch splits the loads).  A null base is an empty range.
+// nv rows of d elements, ld apart; accesses past the last one read zero and
+// store nothing (offsets are range-checked in hardware, so no lane mask or
+// branch splits the loads).  nv <= 0: an empty range (ld >= d there).
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t ld, int nv, int d, int es) {
-  const int bytes = p && nv > 0 ? static_cast<int>(((nv - 1) * ld + d) * es) : 0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, ssm::kBufWord3);
+  const int bytes = ((nv - 1) * static_cast<int>(ld) + d) * es;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes > 0 ? bytes : 0, ssm::kBufWord3);
 }
 
 // Byte offset past any row range (which holds at most 64 x 2^24 bytes).
@@ -247,27 +213,56 @@ struct Tile {
   static constexpr int RPI = kThreads / (D / C::EPV);  // rows a load instruction covers
   typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
   u32x4 r[N];
-  uint32_t voff, step;  // the lane's byte offset; bytes between the rows of successive instructions
+  uint32_t voff;  // the lane's byte offset in an instruction's rows
   int lds_off;
   __device__ __forceinline__ void init(int64_t ld, int d) {
     const int row = threadIdx.x / (D / C::EPV), col = threadIdx.x % (D / C::EPV) * C::EPV;
     voff = col < d ? static_cast<uint32_t>((row * ld + col) * sizeof(T)) : kOutside;
-    step = static_cast<uint32_t>(RPI * ld * sizeof(T));
     lds_off = at<T, D>(row, col);
   }
   __device__ __forceinline__ void load(const T* p, int64_t ld, int nv, int d) {
-    const __amdgpu_buffer_rsrc_t rs = rows_rsrc(p, ld, nv, d, sizeof(T));
+    // one range per instruction (scalar work) keeps it to one lane offset
 #pragma unroll
-    for (int i = 0; i < N; i++) {
-      // a lane past d stays outside: steps stay under 2^30 bytes in all
-      r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, voff + i * step, 0, 0));
-    }
+    for (int i = 0; i < N; i++)
+      r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                          rows_rsrc(p + i * RPI * ld, ld, nv - i * RPI, d, sizeof(T)), voff, 0, 0));
   }
   __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
     for (int i = 0; i < N; i++) *reinterpret_cast<u32x4*>(lds + lds_off + at<T, D>(i * RPI, 0)) = r[i];
   }
 };
+
+// Four elements of a row range as loaded, and as floats.
+template <class T> struct RawRows;
+template <> struct RawRows<float> {
+  typedef f32x4_t type;
+  static __device__ __forceinline__ type load(__amdgpu_buffer_rsrc_t rs, uint32_t voff) {
+    return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0));
+  }
+  static __device__ __forceinline__ f32x4_t f32(type v) { return v; }
+};
+template <> struct RawRows<bf16_t> {
+  typedef uint2 type;
+  static __device__ __forceinline__ type load(__amdgpu_buffer_rsrc_t rs, uint32_t voff) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rs, voff, 0, 0));
+  }
+  static __device__ __forceinline__ f32x4_t f32(type u) {
+    return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                   __uint_as_float(u.y & 0xffff0000u)};
+  }
+};
+
+// Rounds the values to bf16; if more parts follow, leaves what the rounding lost.
+__device__ __forceinline__ bf16x8_t take_part(float (&v)[8], bool more) {
+  bf16x8_t p;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    p[e] = static_cast<__bf16>(v[e]);
+    if (more) v[e] -= static_cast<float>(p[e]);
+  }
+  return p;
+}
 
 // Four output elements at a byte offset of a row range.
 __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, f32x4_t v, float*) {
@@ -278,18 +273,9 @@ __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t v
   typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
   __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, rs, voff, 0, 0);
 }
-__device__ __forceinline__ f32x4_t load_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, const float*) {
-  return __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, voff, 0, 0));
-}
-__device__ __forceinline__ f32x4_t load_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, const bf16_t*) {
-  const auto u = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, 0, 0);
-  return f32x4_t{__uint_as_float(u[0] << 16), __uint_as_float(u[0] & 0xffff0000u), __uint_as_float(u[1] << 16),
-                 __uint_as_float(u[1] & 0xffff0000u)};
-}
-
 // OT: type of the output rows, the io type or float.
 template <class T, class OT, int DM, int DN, bool REV, int MODE>
-__device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
+__device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, int h, char* smem) {
   using C = Cfg<T>;
   using M = Lds<T, DM, DN, MODE>;
   constexpr bool kBf = C::kBf;
@@ -300,15 +286,10 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int l15 = lane & 15, g = lane >> 4;
-  const int h = blockIdx.y;
-  const uint32_t slot = blockIdx.x;
 
   if (!r.K) return;  // a run that this launch leaves out
   Segment sg;
   const bool have = find_segment(a.sq, slot, CH, &sg);
-  if constexpr (MODE == kOutRevDg) {
-    if (r.dg_seg && !have && threadIdx.x == 0) r.dg_seg[static_cast<int64_t>(slot) * a.Hv + h] = 0.0;
-  }
   if (!have) return;
   if (MODE == kAgg && (REV ? sg.first : sg.last)) return;  // nothing after it
 
@@ -321,7 +302,6 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
   float* const sRint = sF + M::red;        // [4][CH]
   float* const sRow = sRint + 4 * CH;      // [JW][CH]
   float* const sCol = sRow + JW * CH;      // [NIB][CH]
-  float* const sDot = sCol + NIB * CH;     // [4]
 
   const int n0 = wave * 16 * NB;  // this wavefront's state columns
 
@@ -378,14 +358,14 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
     if constexpr (MODE != kAgg) tq.load(Qp + tb * r.ldq, r.ldq, n, r.dm);
     tk.load(Kp + tb * r.ldk, r.ldk, n, r.dm);
     tv.load(Vp + tb * r.ldv, r.ldv, n, r.dn);
-    if constexpr (MODE == kOutFwdDg) tx.load(Xp + tb * r.ldx, r.ldx, n, r.dn);
   };
-  // Sums of a chunk's log decays in 64 bits (base 2) and the weights made
-  // from them.  A decay below e^-13000 is taken as that: both are zero in
-  // every product, and -inf would make a NaN of inf - inf.
+  auto issue_x = [&](int c, bool live) {
+    const int64_t tb = sg.t0 + (live ? c * CH : 0);
+    if constexpr (MODE == kOutFwdDg) tx.load(Xp + tb * r.ldx, r.ldx, chunk_rows(c, live), r.dn);
+  };
+  // Sums of a chunk's log decays in 64 bits (base 2) and the weights made from them.
   auto decays = [&](int buf) {
-    const double G =
-        prefix_sum(static_cast<double>(g_next < -13000.0f ? -13000.0f : g_next) * 1.4426950408889634);
+    const double G = prefix_sum(decay_log2(g_next));
     const uint2 gb = __builtin_bit_cast(uint2, G);
     const uint2 tb{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.x), CH - 1)),
                    static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.y), CH - 1))};
@@ -401,16 +381,39 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
     if (lane == 0) sF[M::wc + buf] = exp2_split(tot);
   };
 
-  auto chunk_state = [&](int c) {
-    return reinterpret_cast<f32x4_t*>(r.chunk_states +
-                                      (static_cast<int64_t>(sg.chunk_slot + c) * a.Hv + h) * (DM * DN));
+  // Anchor states and their adjoints lie as the accumulators hold them.
+  auto keep_state = [&](int c) {
+    const int k = nch - 1 - c;
+    if (k % kAnchor) return;
+    f32x4_t* p = reinterpret_cast<f32x4_t*>(
+        r.anchors + ((anchor_slot(sg, slot) + k / kAnchor) * a.Hv + h) * (DM * DN));
+#pragma unroll
+    for (int mb = 0; mb < MB; mb++)
+#pragma unroll
+      for (int nb = 0; nb < NB; nb++) p[(mb * NB + nb) * kThreads + threadIdx.x] = S[mb][nb];
+  };
+
+  auto put = [&](int64_t tb, int nv, const f32x4_t (&Y)[NB][NIB]) {
+    char* const o = static_cast<char*>(r.out) + (tb * r.ldo + h * r.dn) * es_out;
+    const int n_out = r.out ? nv : 0;
+#pragma unroll
+    for (int b = 0; b < NIB; b++) {
+      const __amdgpu_buffer_rsrc_t ro =
+          rows_rsrc(o + 16 * b * r.ldo * es_out, r.ldo, n_out - 16 * b, r.dn, es_out);
+#pragma unroll
+      for (int nb = 0; nb < NB; nb++) {
+        const int n = n0 + 16 * nb + 4 * g;
+        store_rows(ro, n < r.dn ? static_cast<uint32_t>((l15 * r.ldo + n) * es_out) : kOutside, Y[nb][b],
+                   static_cast<OT*>(nullptr));
+      }
+    }
   };
 
   float decay_seg = 1.0f;
-  double dg_sum = 0.0;
   if (nch > 0) {
     issue_decay(REV ? nch - 1 : 0, true);
     issue(REV ? nch - 1 : 0, true);
+    issue_x(REV ? nch - 1 : 0, true);
     if (wave == kDecayWave) decays(0);
     // Global accesses retire in order: the loop waits for its loads by
     // counting what it issued after them.  Wait for the entering state and
@@ -419,12 +422,9 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
     // stores.
     __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     if constexpr (MODE != kAgg) {
-      const __amdgpu_buffer_rsrc_t none = rows_rsrc(nullptr, 0, 0, 0, 0);
+      const __amdgpu_buffer_rsrc_t none = rows_rsrc(a.log_decay, 0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < NB * NIB; i++) store_rows(none, 16 * lane, f32x4_t{0.f, 0.f, 0.f, 0.f}, static_cast<OT*>(nullptr));
-      if constexpr (MODE == kOutFwdDg)
-#pragma unroll
-        for (int i = 0; i < MB * NB; i++) store_rows(none, 16 * lane, f32x4_t{0.f, 0.f, 0.f, 0.f}, static_cast<float*>(nullptr));
     }
   }
   for (int it = 0; it < nch; it++) {
@@ -446,24 +446,19 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
     // this chunk's own waits come first in program order: the next chunk's
     // decays, and the loads that only this chunk uses
     issue_decay(REV ? c - 1 : c + 1, it + 1 < nch);
-    f32x4_t cs[MODE == kOutRevDg ? MB : 1][MODE == kOutRevDg ? NB : 1], xv[MODE == kOutRevDg ? NB : 1][MODE == kOutRevDg ? NIB : 1];
+    typename RawRows<T>::type xv[MODE == kOutRevDg ? NB : 1][MODE == kOutRevDg ? NIB : 1];
     if constexpr (MODE == kOutRevDg) {
-      const f32x4_t* p = chunk_state(c);
 #pragma unroll
-      for (int mb = 0; mb < MB; mb++)
+      for (int b = 0; b < NIB; b++) {
+        const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + (tb + 16 * b) * r.ldx, r.ldx, nv - 16 * b, r.dn, sizeof(T));
 #pragma unroll
-        for (int nb = 0; nb < NB; nb++) cs[mb][nb] = p[(mb * NB + nb) * kThreads + threadIdx.x];
-      const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + tb * r.ldx, r.ldx, nv, r.dn, sizeof(T));
-#pragma unroll
-      for (int nb = 0; nb < NB; nb++) {
-        const int n = n0 + 16 * nb + 4 * g;
-        const uint32_t vo = n < r.dn ? static_cast<uint32_t>((l15 * r.ldx + n) * sizeof(T)) : kOutside;
-#pragma unroll
-        for (int b = 0; b < NIB; b++) xv[nb][b] = load_rows(rx, vo + b * static_cast<uint32_t>(16 * r.ldx * sizeof(T)), Xp);
+        for (int nb = 0; nb < NB; nb++) {
+          const int n = n0 + 16 * nb + 4 * g;
+          xv[nb][b] = RawRows<T>::load(rx, n < r.dn ? static_cast<uint32_t>((l15 * r.ldx + n) * sizeof(T)) : kOutside);
+        }
       }
-    } else {
-      issue(REV ? c - 1 : c + 1, it + 1 < nch);
     }
+    if constexpr (MODE == kAgg) issue(REV ? c - 1 : c + 1, it + 1 < nch);
     const float wc = sF[M::wc + buf];
 
     f32x4_t Y[NB][NIB];
@@ -474,12 +469,20 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
       const int i = 16 * ib + l15;
       const float ghi = gh[i], gli = gl[i];
       float rowsum = 0.0f;
-#pragma unroll
-      for (int jj = 0; jj < NIB / JW; jj++) {
-        const int jb = jj * JW + wave / NIB;
-        f32x4_t p{0.f, 0.f, 0.f, 0.f};
-        float colsum[4] = {0.f, 0.f, 0.f, 0.f};
-        if (REV ? jb >= ib : jb <= ib) {
+      // the blocks that the mask leaves, and zeros in the other block of the
+      // 32 columns that the product with V takes at once
+      if constexpr (kBf) {
+        if ((ib & 1) == (REV ? 1 : 0)) store4(sP + at_p<T>(i, 16 * (REV ? ib - 1 : ib + 1) + 4 * g), f32x4_t{0.f, 0.f, 0.f, 0.f});
+      }
+#pragma unroll 1
+      for (int jb = wave / NIB; jb < NIB; jb += JW) {
+        if (REV ? jb < ib : jb > ib) {
+          if constexpr (MODE == kOutFwdDg) {
+            if (l15 < 4) sCol[ib * CH + 16 * jb + 4 * g + l15] = 0.0f;
+          }
+        } else {
+          f32x4_t p;
+          float colsum[4];
           f32x4_t acc{0.f, 0.f, 0.f, 0.f};
           f32x4_t acx{0.f, 0.f, 0.f, 0.f};
           const int rj = 16 * jb + l15;
@@ -524,13 +527,15 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
               colsum[e] = m;
             }
           }
-        }
-        store4(sP + at_p<T>(i, 16 * jb + 4 * g), p);
-        if constexpr (MODE == kOutFwdDg) {
+          store4(sP + at_p<T>(i, 16 * jb + 4 * g), p);
+          if constexpr (MODE == kOutFwdDg) {
+            float s = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            const float s = sum16(colsum[e]);
-            if (l15 == 0) sCol[ib * CH + 16 * jb + 4 * g + e] = s;
+            for (int e = 0; e < 4; e++) {
+              const float t = sum16(colsum[e]);
+              s = l15 == e ? t : s;
+            }
+            if (l15 < 4) sCol[ib * CH + 16 * jb + 4 * g + l15] = s;
           }
         }
       }
@@ -539,19 +544,9 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
         if (g == 0) sRow[(wave / NIB) * CH + i] = rowsum;
       }
 
-      if constexpr (MODE == kOutRevDg) {
-        // the state entering this chunk meets the adjoint of the one leaving it
-        float dot = 0.0f;
-#pragma unroll
-        for (int mb = 0; mb < MB; mb++)
-#pragma unroll
-          for (int nb = 0; nb < NB; nb++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) dot = fmaf(cs[mb][nb][e], S[mb][nb][e], dot);
-        dot = sum_groups(sum16(dot));
-        if (lane == 0) sDot[wave] = dot;
-        issue(REV ? c - 1 : c + 1, it + 1 < nch);
-      }
+      if constexpr (kDg) keep_state(c);
+      // the next chunk's loads: after the scores, whose registers they take
+      issue(REV ? c - 1 : c + 1, it + 1 < nch);
 
       // the state's part, transposed: rows n of this wavefront, columns i
 #pragma unroll
@@ -561,6 +556,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
       if constexpr (kBf) {
 #pragma unroll
         for (int kb = 0; kb < MB / 2; kb++) {
+          __builtin_amdgcn_sched_barrier(0);
           bf16x8_t qf[NIB];
 #pragma unroll
           for (int b = 0; b < NIB; b++) {
@@ -570,17 +566,14 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
           }
 #pragma unroll
           for (int nb = 0; nb < NB; nb++) {
-            bf16x8_t hi, lo;
+            float s[8];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-              const float s = S[2 * kb + e / 4][nb][e % 4];
-              hi[e] = static_cast<__bf16>(s);
-              if constexpr (kDg) lo[e] = static_cast<__bf16>(s - static_cast<float>(hi[e]));
-            }
+            for (int e = 0; e < 8; e++) s[e] = S[2 * kb + e / 4][nb][e % 4];
 #pragma unroll
-            for (int b = 0; b < NIB; b++) {
-              Y[nb][b] = mfma_bf16(hi, qf[b], Y[nb][b]);
-              if constexpr (kDg) Y[nb][b] = mfma_bf16(lo, qf[b], Y[nb][b]);
+            for (int part = 0; part < (kDg ? kParts : 1); part++) {
+              const bf16x8_t sf = take_part(s, part + 1 < kParts);
+#pragma unroll
+              for (int b = 0; b < NIB; b++) Y[nb][b] = mfma_bf16(sf, qf[b], Y[nb][b]);
             }
           }
         }
@@ -596,6 +589,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
               for (int e = 0; e < 4; e++) Y[nb][b] = mfma_f32(S[mb][nb][e], q[e], Y[nb][b]);
           }
       }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int b = 0; b < NIB; b++) {
         const float w = wq[16 * b + l15];
@@ -609,7 +603,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
             for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
           }
           if constexpr (MODE == kOutRevDg) {
-            const f32x4_t x = xv[nb][b];
+            const f32x4_t x = RawRows<T>::f32(xv[nb][b]);
 #pragma unroll
             for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
           }
@@ -619,18 +613,12 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
           if (g == 0) sRint[wave * CH + 16 * b + l15] = dot;
         }
       }
-      if constexpr (MODE == kOutFwdDg) {
-        // the state entering this chunk, for the reverse run
-        f32x4_t* p = chunk_state(c);
-#pragma unroll
-        for (int mb = 0; mb < MB; mb++)
-#pragma unroll
-          for (int nb = 0; nb < NB; nb++) p[(mb * NB + nb) * kThreads + threadIdx.x] = S[mb][nb];
-      }
     }
     if constexpr (MODE != kAgg) lds_barrier();  // scores and partial sums are in LDS; gh, gl, wq are free
+    issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
     if (wave == kDecayWave && it + 1 < nch) decays(buf ^ 1);
 
+    __builtin_amdgcn_sched_barrier(0);
     // V of this wavefront's columns, tokens along the lane's elements
     if constexpr (kBf) {
       bf16x8_t vf[CH / 32][NB];
@@ -650,7 +638,9 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 #pragma unroll
               for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
             }
+        put(tb, nv, Y);
       }
+      __builtin_amdgcn_sched_barrier(0);
       // the state's update
 #pragma unroll
       for (int mb = 0; mb < MB; mb++)
@@ -658,24 +648,24 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
         for (int nb = 0; nb < NB; nb++) S[mb][nb] = S[mb][nb] * wc;
 #pragma unroll
       for (int kb = 0; kb < CH / 32; kb++) {
+        __builtin_amdgcn_sched_barrier(0);
         const f32x4_t w0 = load4(wk + 32 * kb + 8 * g), w1 = load4(wk + 32 * kb + 8 * g + 4);
-        bf16x8_t hi[NB], lo[NB];
+        bf16x8_t vw[NB][kParts];
 #pragma unroll
-        for (int nb = 0; nb < NB; nb++)
+        for (int nb = 0; nb < NB; nb++) {
+          float u[8];
 #pragma unroll
-          for (int e = 0; e < 8; e++) {
-            const float u = static_cast<float>(vf[kb][nb][e]) * (e < 4 ? w0[e % 4] : w1[e % 4]);
-            hi[nb][e] = static_cast<__bf16>(u);
-            lo[nb][e] = static_cast<__bf16>(u - static_cast<float>(hi[nb][e]));
-          }
+          for (int e = 0; e < 8; e++) u[e] = static_cast<float>(vf[kb][nb][e]) * (e < 4 ? w0[e % 4] : w1[e % 4]);
+#pragma unroll
+          for (int part = 0; part < kParts; part++) vw[nb][part] = take_part(u, part + 1 < kParts);
+        }
 #pragma unroll
         for (int mb = 0; mb < MB; mb++) {
           const bf16x8_t kf = read_tr<DM>(sK, 32 * kb + 8 * g, 16 * mb, l15);
 #pragma unroll
-          for (int nb = 0; nb < NB; nb++) {
-            S[mb][nb] = mfma_bf16(kf, hi[nb], S[mb][nb]);
-            S[mb][nb] = mfma_bf16(kf, lo[nb], S[mb][nb]);
-          }
+          for (int nb = 0; nb < NB; nb++)
+#pragma unroll
+            for (int part = 0; part < kParts; part++) S[mb][nb] = mfma_bf16(kf, vw[nb][part], S[mb][nb]);
         }
       }
     } else {
@@ -712,25 +702,11 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
             for (int nb = 0; nb < NB; nb++) S[mb][nb] = mfma_f32(kf, vf[e][nb] * w[e], S[mb][nb]);
           }
       }
+      if constexpr (MODE != kAgg) put(tb, nv, Y);
     }
     if constexpr (MODE == kAgg) decay_seg *= wc;
 
     if constexpr (MODE != kAgg) {
-      {
-        const int64_t o0 = tb * r.ldo + h * r.dn;
-        char* const ob = r.out ? static_cast<char*>(r.out) + o0 * es_out : nullptr;
-        const __amdgpu_buffer_rsrc_t ro = rows_rsrc(ob, r.ldo, nv, r.dn, es_out);
-#pragma unroll
-        for (int nb = 0; nb < NB; nb++) {
-          const int n = n0 + 16 * nb + 4 * g;
-          const uint32_t vo = n < r.dn ? static_cast<uint32_t>((l15 * r.ldo + n) * es_out) : kOutside;
-#pragma unroll
-          for (int b = 0; b < NIB; b++) {
-            const uint32_t v = vo + b * static_cast<uint32_t>(16 * r.ldo * es_out);
-            store_rows(ro, v, Y[nb][b], static_cast<OT*>(nullptr));
-          }
-        }
-      }
       // one lane per token: the decay gradient's sums inside the chunk
       if constexpr (kDg) {
         if (wave == kDecayWave) {
@@ -742,7 +718,6 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
               for (int w = 0; w < NIB; w++) x -= sCol[w * CH + lane];
             }
           }
-          const int64_t o = (tb + lane) * a.Hv + h;
           if constexpr (MODE == kOutFwdDg) {
             // sums over i >= t
 #pragma unroll
@@ -750,17 +725,10 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
               const double u = __shfl_down(x, d, 64);
               if (lane + d < CH) x += u;
             }
-            if (lane < nv) r.tok[o] = static_cast<float>(x);
           } else {
-            // sums over j < t
-            x = prefix_sum(x) - x;
-            if (lane < nv) {
-              const float dot = (sDot[0] + sDot[1]) + (sDot[2] + sDot[3]);
-              const double dg = x + static_cast<double>(wc * dot) + static_cast<double>(r.tok[o]);
-              if (r.dg_tok) r.dg_tok[o] = static_cast<float>(dg);
-              dg_sum += dg;
-            }
+            x = prefix_sum(x);  // sums over j <= t
           }
+          if (lane < nv) r.tok[static_cast<int64_t>(h) * a.sq.T + tb + lane] = static_cast<float>(x);
         }
       }
     }
@@ -785,13 +753,28 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
           for (int e = 0; e < 4; e++) s_out[(m + e) * r.sm + n * r.sn] = S[mb][nb][e];
       }
   }
-  if constexpr (MODE == kOutRevDg) {
-    if (r.dg_seg && wave == kDecayWave) {
-#pragma unroll
-      for (int d = 32; d >= 1; d >>= 1) dg_sum += __shfl_xor(dg_sum, d, 64);
-      if (lane == 0) r.dg_seg[static_cast<int64_t>(slot) * a.Hv + h] = dg_sum;
-    }
-  }
+}
+
+// The workgroup's segment, head and run.  Workgroups go round-robin over the
+// 8 XCDs; the runs of one head, which read the same rows, and with enough of
+// them the heads that share q and k, follow one another on one XCD and find
+// the rows in its L2.
+struct Work {
+  uint32_t slot;
+  int h, z;
+  bool any;
+};
+
+__device__ __forceinline__ Work work_of(const Args& a, int nz) {
+  const uint32_t unit_wgs = static_cast<uint32_t>(a.unit_heads * nz);
+  const uint32_t i = blockIdx.x / 8, u = i / unit_wgs * 8 + blockIdx.x % 8, k = i % unit_wgs;
+  const uint32_t per_slot = static_cast<uint32_t>(a.Hv / a.unit_heads);
+  Work w;
+  w.any = u < a.units;
+  w.slot = u / per_slot;
+  w.h = static_cast<int>(u % per_slot * a.unit_heads + k / nz);
+  w.z = static_cast<int>(k % nz);
+  return w;
 }
 
 // Kinds: kGrad... with PT the type of dq and dk, float where the value heads
@@ -799,20 +782,19 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, char* smem) {
 template <class T, class PT, int DK, int DV, int KIND>
 __global__ __launch_bounds__(kThreads, 2) void k_linattn(Args a) {
   extern __shared__ __attribute__((aligned(16))) char smem_la[];
+  const Work w = work_of(a, a.nz);
+  if (!w.any) return;
+  const Run& r = a.run[w.z];
   if constexpr (KIND == kForward) {
-    run<T, T, DK, DV, false, kOut>(a, a.run[0], smem_la);
+    run<T, T, DK, DV, false, kOut>(a, r, w.slot, w.h, smem_la);
   } else if constexpr (KIND == kAggregate) {
-    if (blockIdx.z == 0) run<T, T, DK, DV, false, kAgg>(a, a.run[0], smem_la);
-    else run<T, T, DK, DV, true, kAgg>(a, a.run[1], smem_la);
-  } else if constexpr (KIND == kGradFirst) {
-    if (blockIdx.z == 0) run<T, PT, DV, DK, false, kOutFwdDg>(a, a.run[0], smem_la);
-    else run<T, T, DK, DV, true, kOut>(a, a.run[1], smem_la);
-  } else if constexpr (KIND == kGradSecond) {
-    run<T, PT, DV, DK, true, kOutRevDg>(a, a.run[0], smem_la);
+    if (w.z == 0) run<T, T, DK, DV, false, kAgg>(a, r, w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kAgg>(a, r, w.slot, w.h, smem_la);
   } else {
-    if (blockIdx.z == 0) run<T, PT, DV, DK, false, kOut>(a, a.run[0], smem_la);
-    else if (blockIdx.z == 1) run<T, T, DK, DV, true, kOut>(a, a.run[1], smem_la);
-    else run<T, PT, DV, DK, true, kOut>(a, a.run[2], smem_la);
+    constexpr bool dg = KIND == kGradDecay;
+    if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut>(a, r, w.slot, w.h, smem_la);
+    else if (w.z == 1) run<T, PT, DV, DK, true, dg ? kOutRevDg : kOut>(a, r, w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kOut>(a, r, w.slot, w.h, smem_la);
   }
 }
 
@@ -822,13 +804,12 @@ template <class T, int DK, int DV, int KIND>
 constexpr int lds_bytes() {
   if (KIND == kForward) return Lds<T, DK, DV, kOut>::bytes;
   if (KIND == kAggregate) return Lds<T, DK, DV, kAgg>::bytes;
-  if (KIND == kGradFirst) return max2(Lds<T, DV, DK, kOutFwdDg>::bytes, Lds<T, DK, DV, kOut>::bytes);
-  if (KIND == kGradSecond) return Lds<T, DV, DK, kOutRevDg>::bytes;
+  if (KIND == kGradDecay) return max2(Lds<T, DV, DK, kOutFwdDg>::bytes, Lds<T, DK, DV, kOut>::bytes);
   return max2(Lds<T, DV, DK, kOut>::bytes, Lds<T, DK, DV, kOut>::bytes);
 }
 
 template <class T, class PT, int DK, int DV, int KIND>
-hipError_t launch_one(const Args& a, int nz, hipStream_t st) {
+hipError_t launch_one(const Args& a, hipStream_t st) {
   constexpr int lds = lds_bytes<T, DK, DV, KIND>();
   static_assert(lds <= 80 * 1024, "two workgroups share a CU's 160 KB");
   auto kern = k_linattn<T, PT, DK, DV, KIND>;
@@ -837,25 +818,19 @@ hipError_t launch_one(const Args& a, int nz, hipStream_t st) {
         hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  const dim3 grid(static_cast<unsigned>(slot_count(a.sq.T, a.sq.S, a.sq.L)), static_cast<unsigned>(a.Hv),
-                  static_cast<unsigned>(nz));
+  const uint32_t grid = (a.units + 7) / 8 * 8 * static_cast<uint32_t>(a.unit_heads * a.nz);
   kern<<<grid, kThreads, lds, st>>>(a);
   return hipGetLastError();
 }
 
-template <class T, class PT, int DK, int DV>
-hipError_t launch_grad(Kernel k, const Args& a, int nz, hipStream_t st) {
-  if (k == kGradFirst) return launch_one<T, PT, DK, DV, kGradFirst>(a, nz, st);
-  if (k == kGradSecond) return launch_one<T, PT, DK, DV, kGradSecond>(a, nz, st);
-  return launch_one<T, PT, DK, DV, kGradPlain>(a, nz, st);
-}
-
 template <class T, int DK, int DV>
-hipError_t launch_kind(Kernel k, const Args& a, int nz, hipStream_t st) {
-  if (k == kForward) return launch_one<T, T, DK, DV, kForward>(a, nz, st);
-  if (k == kAggregate) return launch_one<T, T, DK, DV, kAggregate>(a, nz, st);
-  if (a.sum_heads) return launch_grad<T, float, DK, DV>(k, a, nz, st);
-  return launch_grad<T, T, DK, DV>(k, a, nz, st);
+hipError_t launch_kind(Kernel k, const Args& a, hipStream_t st) {
+  if (k == kForward) return launch_one<T, T, DK, DV, kForward>(a, st);
+  if (k == kAggregate) return launch_one<T, T, DK, DV, kAggregate>(a, st);
+  if (a.sum_heads)
+    return k == kGradDecay ? launch_one<T, float, DK, DV, kGradDecay>(a, st)
+                           : launch_one<T, float, DK, DV, kGradPlain>(a, st);
+  return k == kGradDecay ? launch_one<T, T, DK, DV, kGradDecay>(a, st) : launch_one<T, T, DK, DV, kGradPlain>(a, st);
 }
 
 }  // namespace

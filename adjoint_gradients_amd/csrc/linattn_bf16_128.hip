@@ -4,9 +4,9 @@
 
 namespace la {
 
-hipError_t launch_bf16_128(Kernel k, int dv, const Args& a, int nz, hipStream_t st) {
-  if (padded(dv) == 64) return launch_kind<ssm::bf16_t, 128, 64>(k, a, nz, st);
-  return launch_kind<ssm::bf16_t, 128, 128>(k, a, nz, st);
+hipError_t launch_bf16_128(Kernel k, int dv, const Args& a, hipStream_t st) {
+  if (padded(dv) == 64) return launch_kind<ssm::bf16_t, 128, 64>(k, a, st);
+  return launch_kind<ssm::bf16_t, 128, 128>(k, a, st);
 }
 
 }  // namespace la

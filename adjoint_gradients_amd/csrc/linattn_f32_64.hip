@@ -4,9 +4,9 @@
 
 namespace la {
 
-hipError_t launch_f32_64(Kernel k, int dv, const Args& a, int nz, hipStream_t st) {
-  if (padded(dv) == 64) return launch_kind<float, 64, 64>(k, a, nz, st);
-  return launch_kind<float, 64, 128>(k, a, nz, st);
+hipError_t launch_f32_64(Kernel k, int dv, const Args& a, hipStream_t st) {
+  if (padded(dv) == 64) return launch_kind<float, 64, 64>(k, a, st);
+  return launch_kind<float, 64, 128>(k, a, st);
 }
 
 }  // namespace la
