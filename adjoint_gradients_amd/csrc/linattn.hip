@@ -332,19 +332,22 @@ ssm_status check_in(const ssm_linattn_dims* d, const ssm_linattn_in* in) {
   return SSM_OK;
 }
 
-// Tokens per segment.  A run walks its segment chunk by chunk, so segments
-// are made short enough for kTargetWgs workgroups, but of at least kMinChunks
-// chunks: a segment costs one more read of two of its operands and two
-// passes over a state.  Without room for two segments there is one per
-// sequence, and neither of those passes.
-constexpr int64_t kTargetWgs = 1024;
+// Tokens per segment.  A run walks its segment chunk by chunk.  Segments are
+// short enough for kRounds workgroups for each that fits on the chip at once
+// (some take a third longer than others, and the last round hides it), but of
+// at least kMinChunks chunks: a segment costs one more read of two of its
+// operands and two passes over a state.  Without room for two segments there
+// is one per sequence, and neither of those passes.
+constexpr int64_t kCus = 256;
+constexpr int64_t kRounds = 4;
 constexpr int64_t kMinChunks = 4;
 
 int64_t longest(const ssm_linattn_dims* d, bool packed) { return packed ? d->T : d->T / d->S; }
 
 int64_t segment_tokens(const ssm_linattn_dims* d, bool packed, int runs) {
   const int64_t ch = chunk_tokens(d->io == SSM_BF16);
-  int64_t L = (d->T * d->Hv * runs / kTargetWgs + ch - 1) / ch * ch;
+  const int64_t wgs = kRounds * kCus * (padded(d->dk) * padded(d->dv) > 64 * 64 ? 2 : 3);
+  int64_t L = (d->T * d->Hv * runs / wgs + ch - 1) / ch * ch;
   if (L < kMinChunks * ch) L = kMinChunks * ch;
   const int64_t n = (longest(d, packed) + ch - 1) / ch * ch;
   return L < n ? L : n;
@@ -420,11 +423,14 @@ size_t plan_bytes(const ssm_linattn_dims* d, const ssm_linattn_grads* g) {
 
 bool any_grad(const ssm_linattn_grads* g) { return g->dq || g->dk || g->dv || g->dlog_decay || g->dh0; }
 
-hipError_t launch(Kernel k, const ssm_linattn_dims* d, Args& a, int nz, hipStream_t st) {
+// Launches the runs of a kernel that have operands.
+hipError_t launch(Kernel k, const ssm_linattn_dims* d, Args& a, hipStream_t st) {
   // Heads that share q and k stay on one XCD where that still leaves each of
   // the 8 XCDs several units of work.
   const int64_t slots = slot_count(d->T, d->S, a.sq.L);
-  a.nz = nz;
+  a.nz = 0;
+  for (int i = 0; i < 3; i++)
+    if (a.run[i].K) a.run_of[a.nz++] = i;
   a.unit_heads = slots * d->Hk >= 64 ? d->Hv / d->Hk : 1;
   a.units = static_cast<uint32_t>(slots * (d->Hv / a.unit_heads));
   const bool wide = padded(d->dk) == 128;
@@ -471,7 +477,7 @@ hipError_t carry_states(const ssm_linattn_dims* d, Args a, const Run& fwd, const
     a.run[i].sm = d->dv;
     a.run[i].sn = 1;
   }
-  hipError_t e = launch(kAggregate, d, a, w.seg[1] ? 2 : 1, st);
+  hipError_t e = launch(kAggregate, d, a, st);
   if (e != hipSuccess) return e;
   CarryArgs c{};
   c.sq = a.sq;
@@ -510,7 +516,7 @@ hipError_t run_forward(const ssm_linattn_dims* d, const ssm_linattn_in* in, void
   r.out = y;
   r.ldo = ldy;
   a.run[0] = r;
-  return launch(kForward, d, a, 1, st);
+  return launch(hT ? kForwardState : kForward, d, a, st);
 }
 
 hipError_t group_sum(const ssm_linattn_dims* d, const Seqs& sq, const float* part, void* out, hipStream_t st) {
@@ -534,7 +540,6 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   Args a = base_args(d, in, p);
   hipError_t e;
   if (p.split) {
-    // an unused direction has no operands and exits at once
     const Run fwd = p.need_s ? make_run(k, k, v, 1.0f, 1.0f) : Run{};
     const Run rev = p.need_d ? make_run(q, q, o, 1.0f, d->scale) : Run{};
     if ((e = carry_states(d, a, fwd, rev, w, in->h0, dhT, st)) != hipSuccess) return e;
@@ -567,14 +572,12 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   rk.ldo = part_ld;
   rk.tok = w.tok[1];
   rk.anchors = w.anchors[1];
-  const bool need_k = g->dk || p.dg;
-  if (need_k) rk.s_end = g->dh0;
-  else rv.s_end = g->dh0;
-  const bool need_v = g->dv || (!need_k && g->dh0);
+  const bool need_k = g->dk || g->dh0 || p.dg;
+  rk.s_end = g->dh0;
   a.run[0] = g->dq || p.dg ? rq : Run{};
   a.run[1] = need_k ? rk : Run{};
-  a.run[2] = need_v ? rv : Run{};
-  if ((e = launch(p.dg ? kGradDecay : kGradPlain, d, a, need_v ? 3 : 2, st)) != hipSuccess) return e;
+  a.run[2] = g->dv ? rv : Run{};
+  if ((e = launch(p.dg ? kGradDecay : kGradPlain, d, a, st)) != hipSuccess) return e;
   if (p.dg) {
     const DecayArgs da{a.sq, d->Hv, chunk_tokens(d->io == SSM_BF16),
                        static_cast<int32_t>(state_floats(d->dk, d->dv) / 4), in->log_decay, a.ld_decay, w.tok[0],

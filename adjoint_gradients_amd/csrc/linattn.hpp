@@ -47,7 +47,8 @@ struct Args {
   const float* log_decay;
   int64_t ld_decay;                // Hv, or 0 for one decay per head
   int32_t sum_heads;               // dq and dk are float32, one per value head
-  int32_t nz;                      // runs of the launch
+  int32_t nz;                      // runs of the launch,
+  int32_t run_of[3];               // and which they are
   int32_t unit_heads;              // consecutive heads whose workgroups stay on one XCD
   uint32_t units;                  // segment slots x Hv / unit_heads
   Run run[3];
@@ -55,8 +56,9 @@ struct Args {
 
 enum Kernel {
   kForward,    // run 0: y
+  kForwardState,  // the same where the final state is an output too
   kAggregate,  // run 0: the segments' state sums, forward in time; run 1: in reverse
-  kGradPlain,  // runs 0, 1, 2: dq, dk, dv (a run without operands is left out)
+  kGradPlain,  // runs 0, 1, 2: dq, dk (and the adjoint of h0), dv
   kGradDecay   // the same with the decay gradient's terms
 };
 

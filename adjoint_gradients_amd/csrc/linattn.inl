@@ -49,6 +49,7 @@ namespace {
 using ssm::bf16_t;
 using ssm::bf16x8_t;
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4_t;
+typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4_t;
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) v4s lds_v4s;
 
@@ -71,35 +72,40 @@ struct Cfg {
   static constexpr int NIB = CH / 16;      // 16-token blocks
   static constexpr int JW = 4 / NIB;       // wavefronts sharing a row block of the scores
   static constexpr int EPV = 16 / sizeof(T);
+  static constexpr int kPad = kBf ? 16 : 4;  // elements between the rows of a tile (see at())
 };
 
 // LDS of a run, in bytes.
 template <class T, int DM, int DN, int MODE>
 struct Lds {
   using C = Cfg<T>;
-  static constexpr int PM = DM + C::EPV, PN = DN + C::EPV;
+  static constexpr int PM = DM + C::kPad, PN = DN + C::kPad;
   static constexpr int q = 0;
   static constexpr int k = q + (MODE == kAgg ? 0 : C::CH * PM * (int)sizeof(T));
   static constexpr int v = k + C::CH * PM * (int)sizeof(T);
-  static constexpr int x = v + C::CH * PN * (int)sizeof(T);
-  static constexpr int p = x + (MODE == kOutFwdDg ? C::CH * PN * (int)sizeof(T) : 0);
+  static constexpr int p = v + C::CH * PN * (int)sizeof(T);
   static constexpr int f = p + (MODE == kAgg ? 0 : C::CH * C::CH * (int)sizeof(T));
-  // gh, gl, wq; two buffers of wk and of wc; then the decay gradient's partial sums
-  static constexpr int wk = 3 * C::CH;
-  static constexpr int wc = wk + 2 * C::CH;
+  // two buffers of gh, gl, wq, wk and of wc; then the decay gradient's partial sums
+  static constexpr int kDecay = 4 * C::CH;
+  static constexpr int wc = 2 * kDecay;
   static constexpr int red = wc + 4;
-  static constexpr int floats = red + (MODE >= kOutFwdDg ? (4 + C::JW + C::NIB) * C::CH : 0);
+  static constexpr int kSums = (4 + C::JW + C::NIB) * C::CH;  // two buffers of them too
+  static constexpr int floats = red + (MODE >= kOutFwdDg ? 2 * kSums : 0);
   static constexpr int bytes = f + floats * 4;
 };
 
-// Element (r, c) of a tile of D columns in LDS.  Rows start 16 bytes later in
-// the banks than the row before: 16 rows read at one chunk of 16 bytes, or at
-// half a chunk, meet every bank equally often, and every address is one lane
-// offset plus a constant.  (The transposing reads meet half the banks twice;
-// a permutation of the chunks avoids that but needs an address of its own
-// for most reads, about a hundred registers.)
+// Element (r, c) of a tile of D columns in LDS.  bf16: a row starts 8 banks
+// after the row before, and rows 8-15 of 16 swap the 16-byte chunks of each
+// pair.  Then 16 rows read at one chunk, or at half a chunk, and, transposing,
+// 8 rows of two chunks each meet every bank equally often, and every address
+// is one lane offset plus a constant.  fp32: 4 banks further a row, for 16
+// rows of one chunk and for rows e, 4 + e, 8 + e, 12 + e of four.
 template <class T, int D>
-__device__ __forceinline__ int at(int r, int c) { return r * (D + Cfg<T>::EPV) + c; }
+__device__ __forceinline__ int at(int r, int c) {
+  constexpr int EPV = Cfg<T>::EPV;
+  if constexpr (Cfg<T>::kBf) return r * (D + Cfg<T>::kPad) + ((c / EPV) ^ ((r >> 3) & 1)) * EPV + c % EPV;
+  return r * (D + Cfg<T>::kPad) + c;
+}
 
 // Element (i, j) of the scores, without padding (two workgroups a CU need the
 // space): a row's 16-byte chunks are permuted instead.
@@ -137,6 +143,14 @@ __device__ __forceinline__ double prefix_sum(double v) {
   return v;
 }
 
+// A lane's 64-bit value, for all.
+__device__ __forceinline__ double last_lane(double v, int lane) {
+  const uint2 u = __builtin_bit_cast(uint2, v);
+  const uint2 r{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u.x), lane)),
+                static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u.y), lane))};
+  return __builtin_bit_cast(double, r);
+}
+
 template <int CTRL>
 __device__ __forceinline__ float dpp_add(float v) {
   return v + __builtin_bit_cast(
@@ -170,8 +184,11 @@ __device__ __forceinline__ f32x4_t load4(const bf16_t* p) {
   return f32x4_t{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                  __uint_as_float(u.y & 0xffff0000u)};
 }
+// Two floats as bf16 (round to nearest, ties to even): one instruction.
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return static_cast<uint32_t>(ssm::f32_to_bf16(a)) | (static_cast<uint32_t>(ssm::f32_to_bf16(b)) << 16);
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 __device__ __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
 __device__ __forceinline__ void store4(bf16_t* p, f32x4_t v) {
@@ -179,18 +196,23 @@ __device__ __forceinline__ void store4(bf16_t* p, f32x4_t v) {
 }
 
 __device__ __forceinline__ bf16x8_t load8(const bf16_t* p) { return *reinterpret_cast<const bf16x8_t*>(p); }
+__device__ __forceinline__ bf16x8_t load44(const bf16_t* a, const bf16_t* b) {
+  return __builtin_bit_cast(bf16x8_t,
+                            (Pair64{*reinterpret_cast<const uint2*>(a), *reinterpret_cast<const uint2*>(b)}));
+}
 __device__ __forceinline__ bf16x8_t load8(const float*) { return bf16x8_t{}; }  // not reached
 
-// Rows t0 .. t0 + 7 (t0 a multiple of 8, one per 16-lane group) of column
-// c0 + l15: two transposing reads, in which lane s of a group supplies the
-// address of row s / 4, columns 4 (s % 4) .. + 3, and receives column s of
-// the four rows.
+// Column c0 + l15 of rows t0 + 4 g .. + 3 and t0 + 16 + 4 g .. + 3 (t0 a
+// multiple of 32): two transposing reads, in which lane s of a 16-lane group
+// supplies the address of row s / 4, columns 4 (s % 4) .. + 3, and receives
+// column s of the four rows.
 template <int D>
-__device__ __forceinline__ bf16x8_t read_tr(bf16_t* tile, int t0, int c0, int l15) {
-  const int r = t0 + (l15 >> 2), c = c0 + 4 * (l15 & 3);
-  const PairV4 p{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + at<bf16_t, D>(r, c))),
-                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(tile + at<bf16_t, D>(r + 4, c)))};
-  return __builtin_bit_cast(bf16x8_t, p);
+__device__ __forceinline__ bf16x8_t read_tr(bf16_t* tile, int t0, int c0, int lane) {
+  const int s = lane & 15, r = 4 * (lane >> 4) + (s >> 2), c = 4 * (s & 3);
+  bf16_t* const p = tile + at<bf16_t, D>(r, c) + t0 * (D + Cfg<bf16_t>::kPad) + c0;
+  const PairV4 v{__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)p),
+                 __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s*)(p + 16 * (D + Cfg<bf16_t>::kPad)))};
+  return __builtin_bit_cast(bf16x8_t, v);
 }
 
 // nv rows of d elements, ld apart; accesses past the last one read zero and
@@ -211,8 +233,7 @@ struct Tile {
   using C = Cfg<T>;
   static constexpr int N = C::CH * D / C::EPV / kThreads;
   static constexpr int RPI = kThreads / (D / C::EPV);  // rows a load instruction covers
-  typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
-  u32x4 r[N];
+  u32x4_t r[N];
   uint32_t voff;  // the lane's byte offset in an instruction's rows
   int lds_off;
   __device__ __forceinline__ void init(int64_t ld, int d) {
@@ -224,12 +245,12 @@ struct Tile {
     // one range per instruction (scalar work) keeps it to one lane offset
 #pragma unroll
     for (int i = 0; i < N; i++)
-      r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+      r[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
                                           rows_rsrc(p + i * RPI * ld, ld, nv - i * RPI, d, sizeof(T)), voff, 0, 0));
   }
   __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
-    for (int i = 0; i < N; i++) *reinterpret_cast<u32x4*>(lds + lds_off + at<T, D>(i * RPI, 0)) = r[i];
+    for (int i = 0; i < N; i++) *reinterpret_cast<u32x4_t*>(lds + lds_off + at<T, D>(i * RPI, 0)) = r[i];
   }
 };
 
@@ -253,15 +274,24 @@ template <> struct RawRows<bf16_t> {
   }
 };
 
-// Rounds the values to bf16; if more parts follow, leaves what the rounding lost.
+__device__ __forceinline__ float widen(bf16x8_t v, int e) {
+  const uint32_t u = __builtin_bit_cast(u32x4_t, v)[e / 2];
+  return __uint_as_float(e % 2 ? u & 0xffff0000u : u << 16);
+}
+
+// Rounds the values to bf16; if more parts follow, leaves what the rounding
+// lost.  In pairs: one conversion, and each half widened by a shift or a mask.
 __device__ __forceinline__ bf16x8_t take_part(float (&v)[8], bool more) {
-  bf16x8_t p;
+  u32x4_t p;
 #pragma unroll
-  for (int e = 0; e < 8; e++) {
-    p[e] = static_cast<__bf16>(v[e]);
-    if (more) v[e] -= static_cast<float>(p[e]);
+  for (int i = 0; i < 4; i++) {
+    p[i] = pack2(v[2 * i], v[2 * i + 1]);
+    if (more) {
+      v[2 * i] -= __uint_as_float(p[i] << 16);
+      v[2 * i + 1] -= __uint_as_float(p[i] & 0xffff0000u);
+    }
   }
-  return p;
+  return __builtin_bit_cast(bf16x8_t, p);
 }
 
 // Four output elements at a byte offset of a row range.
@@ -273,8 +303,10 @@ __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t v
   typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
   __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, rs, voff, 0, 0);
 }
-// OT: type of the output rows, the io type or float.
-template <class T, class OT, int DM, int DN, bool REV, int MODE>
+// OT: type of the output rows, the io type or float.  PARTS: bf16 parts of
+// the weighted V in the state's update, kParts where the state is an fp32
+// output, two (2^-17) where it only reaches bf16 outputs.
+template <class T, class OT, int DM, int DN, bool REV, int MODE, int PARTS>
 __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, int h, char* smem) {
   using C = Cfg<T>;
   using M = Lds<T, DM, DN, MODE>;
@@ -287,7 +319,6 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int l15 = lane & 15, g = lane >> 4;
 
-  if (!r.K) return;  // a run that this launch leaves out
   Segment sg;
   const bool have = find_segment(a.sq, slot, CH, &sg);
   if (!have) return;
@@ -296,13 +327,8 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   T* const sQ = reinterpret_cast<T*>(smem + M::q);
   T* const sK = reinterpret_cast<T*>(smem + M::k);
   T* const sV = reinterpret_cast<T*>(smem + M::v);
-  T* const sX = reinterpret_cast<T*>(smem + M::x);
   T* const sP = reinterpret_cast<T*>(smem + M::p);
   float* const sF = reinterpret_cast<float*>(smem + M::f);
-  float* const sRint = sF + M::red;        // [4][CH]
-  float* const sRow = sRint + 4 * CH;      // [JW][CH]
-  float* const sCol = sRow + JW * CH;      // [NIB][CH]
-
   const int n0 = wave * 16 * NB;  // this wavefront's state columns
 
   // the state entering the segment
@@ -313,16 +339,25 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     if (split) s_in = r.seg + (static_cast<int64_t>(slot) * a.Hv + h) * a.dkdv;
     else if (r.s0) s_in = r.s0 + (static_cast<int64_t>(sg.seq) * a.Hv + h) * a.dkdv;
   }
+  // a state in memory: element (m, n) at m sm + n sn
+  auto state_rsrc = [&](const float* p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, p ? a.dkdv * 4 : 0, ssm::kBufWord3);
+  };
+  auto state_off = [&](int mb, int nb) {
+    const int m = 16 * mb + 4 * g, n = n0 + 16 * nb + l15;
+    return m < r.dm && n < r.dn ? static_cast<uint32_t>(m * r.sm + n * r.sn) * 4u : kOutside;
+  };
+  {
+    const __amdgpu_buffer_rsrc_t rs = state_rsrc(s_in);
 #pragma unroll
-  for (int mb = 0; mb < MB; mb++)
+    for (int mb = 0; mb < MB; mb++)
 #pragma unroll
-    for (int nb = 0; nb < NB; nb++) {
-      const int m = 16 * mb + 4 * g, n = n0 + 16 * nb + l15;
-      S[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if (s_in && m < r.dm && n < r.dn)
+      for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) S[mb][nb][e] = s_in[(m + e) * r.sm + n * r.sn];
-    }
+        for (int e = 0; e < 4; e++)
+          S[mb][nb][e] = __uint_as_float(
+              __builtin_amdgcn_raw_buffer_load_b32(rs, state_off(mb, nb) + static_cast<uint32_t>(e * r.sm) * 4u, 0, 0));
+  }
 
   const int len = sg.t1 - sg.t0;
   const int nch = (len + CH - 1) / CH;
@@ -332,11 +367,13 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   const T* const Xp = kDg ? static_cast<const T*>(r.X) + (h / r.gv) * r.dn : nullptr;
 
   Tile<T, DM> tq, tk;
-  Tile<T, DN> tv, tx;
+  Tile<T, DN> tv;
+  // rows of X, of this wavefront's row block, as operands of the scores
+  constexpr int XF = MODE == kOutFwdDg ? DN * (int)sizeof(T) / 64 : 1;
+  u32x4_t xf[XF];
   if constexpr (MODE != kAgg) tq.init(r.ldq, r.dm);
   tk.init(r.ldk, r.dm);
   tv.init(r.ldv, r.dn);
-  if constexpr (MODE == kOutFwdDg) tx.init(r.ldx, r.dn);
   constexpr int es_out = sizeof(OT);
   float g_next;  // this lane's log decay of the chunk being loaded
   // Loads of chunk c into registers; past the segment's end (the walk's last
@@ -360,23 +397,32 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     tv.load(Vp + tb * r.ldv, r.ldv, n, r.dn);
   };
   auto issue_x = [&](int c, bool live) {
-    const int64_t tb = sg.t0 + (live ? c * CH : 0);
-    if constexpr (MODE == kOutFwdDg) tx.load(Xp + tb * r.ldx, r.ldx, chunk_rows(c, live), r.dn);
+    if constexpr (MODE == kOutFwdDg) {
+      const int row0 = 16 * (wave % NIB);
+      const int64_t tb = sg.t0 + (live ? c * CH : 0) + row0;
+      const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + tb * r.ldx, r.ldx, chunk_rows(c, live) - row0, r.dn, sizeof(T));
+#pragma unroll
+      for (int i = 0; i < XF; i++) {
+        const int col = (4 * i + g) * C::EPV;
+        xf[i] = __builtin_bit_cast(
+            u32x4_t,
+            __builtin_amdgcn_raw_buffer_load_b128(
+                rx, col < r.dn ? static_cast<uint32_t>((l15 * r.ldx + col) * sizeof(T)) : kOutside, 0, 0));
+      }
+    }
   };
   // Sums of a chunk's log decays in 64 bits (base 2) and the weights made from them.
   auto decays = [&](int buf) {
     const double G = prefix_sum(decay_log2(g_next));
-    const uint2 gb = __builtin_bit_cast(uint2, G);
-    const uint2 tb{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.x), CH - 1)),
-                   static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(gb.y), CH - 1))};
-    const double tot = __builtin_bit_cast(double, tb);
+    const double tot = last_lane(G, CH - 1);
     if (lane < CH) {
+      float* const o = sF + buf * M::kDecay;
       const float hi = static_cast<float>(G);
-      sF[lane] = hi;
-      sF[CH + lane] = static_cast<float>(G - static_cast<double>(hi));
+      o[lane] = hi;
+      o[CH + lane] = static_cast<float>(G - static_cast<double>(hi));
       const float eg = exp2_split(G), er = exp2_split(tot - G);
-      sF[2 * CH + lane] = r.qs * (REV ? er : eg);
-      sF[M::wk + buf * CH + lane] = r.ks * (REV ? eg : er);
+      o[2 * CH + lane] = r.qs * (REV ? er : eg);
+      o[3 * CH + lane] = r.ks * (REV ? eg : er);
     }
     if (lane == 0) sF[M::wc + buf] = exp2_split(tot);
   };
@@ -385,12 +431,14 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   auto keep_state = [&](int c) {
     const int k = nch - 1 - c;
     if (k % kAnchor) return;
-    f32x4_t* p = reinterpret_cast<f32x4_t*>(
-        r.anchors + ((anchor_slot(sg, slot) + k / kAnchor) * a.Hv + h) * (DM * DN));
+    const __amdgpu_buffer_rsrc_t ra =
+        rows_rsrc(r.anchors + ((anchor_slot(sg, slot) + k / kAnchor) * a.Hv + h) * (DM * DN), 0, 1, DM * DN, 4);
 #pragma unroll
     for (int mb = 0; mb < MB; mb++)
 #pragma unroll
-      for (int nb = 0; nb < NB; nb++) p[(mb * NB + nb) * kThreads + threadIdx.x] = S[mb][nb];
+      for (int nb = 0; nb < NB; nb++)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, S[mb][nb]), ra, threadIdx.x * 16,
+                                               (mb * NB + nb) * kThreads * 16, 0);
   };
 
   auto put = [&](int64_t tb, int nv, const f32x4_t (&Y)[NB][NIB]) {
@@ -407,6 +455,28 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
                    static_cast<OT*>(nullptr));
       }
     }
+  };
+
+  // One lane per token: the decay gradient's sums inside chunk c, over i >= t
+  // (forward run) or j <= t (reverse run).
+  auto token_sums = [&](int c, int buf) {
+    const float* const rint = sF + M::red + buf * M::kSums;
+    double x = 0.0;
+    if (lane < CH) {
+#pragma unroll
+      for (int w = 0; w < 4; w++) x += rint[w * CH + lane];
+      if constexpr (MODE == kOutFwdDg) {
+#pragma unroll
+        for (int w = 0; w < JW; w++) x += rint[(4 + w) * CH + lane];
+#pragma unroll
+        for (int w = 0; w < NIB; w++) x -= rint[(4 + JW + w) * CH + lane];
+      }
+    }
+    const double before = prefix_sum(x);
+    if constexpr (MODE == kOutFwdDg) x += last_lane(before, CH - 1) - before;
+    else x = before;
+    const int t = sg.t0 + c * CH + lane;
+    if (lane < CH && t < sg.t1) r.tok[static_cast<int64_t>(h) * a.sq.T + t] = static_cast<float>(x);
   };
 
   float decay_seg = 1.0f;
@@ -432,37 +502,42 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     const int64_t tb = sg.t0 + static_cast<int64_t>(c) * CH;
     const int nv = sg.t1 - static_cast<int>(tb) < CH ? sg.t1 - static_cast<int>(tb) : CH;
     const int buf = it & 1;
-    const float* const gh = sF;
-    const float* const gl = sF + CH;
-    const float* const wq = sF + 2 * CH;
-    const float* const wk = sF + M::wk + buf * CH;
+    int lane_now = lane;
+    if constexpr (kDg) asm volatile("" : "+v"(lane_now));
+    const int l15 = lane_now & 15, g = lane_now >> 4;
+    const float* const gh = sF + buf * M::kDecay;
+    const float* const gl = gh + CH;
+    const float* const wq = gh + 2 * CH;
+    const float* const wk = gh + 3 * CH;
+    float* const sRint = sF + M::red + (kDg ? buf * M::kSums : 0);  // [4][CH]
+    float* const sRow = sRint + 4 * CH;                            // [JW][CH]
+    float* const sCol = sRow + JW * CH;                            // [NIB][CH]
 
     if (it > 0) lds_barrier();  // the previous chunk's readers are done
     if constexpr (MODE != kAgg) tq.store(sQ);
     tk.store(sK);
     tv.store(sV);
-    if constexpr (MODE == kOutFwdDg) tx.store(sX);
     lds_barrier();
-    // this chunk's own waits come first in program order: the next chunk's
-    // decays, and the loads that only this chunk uses
+    // what this chunk waits for comes before the next one's loads
     issue_decay(REV ? c - 1 : c + 1, it + 1 < nch);
-    typename RawRows<T>::type xv[MODE == kOutRevDg ? NB : 1][MODE == kOutRevDg ? NIB : 1];
-    if constexpr (MODE == kOutRevDg) {
-#pragma unroll
-      for (int b = 0; b < NIB; b++) {
-        const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + (tb + 16 * b) * r.ldx, r.ldx, nv - 16 * b, r.dn, sizeof(T));
-#pragma unroll
-        for (int nb = 0; nb < NB; nb++) {
-          const int n = n0 + 16 * nb + 4 * g;
-          xv[nb][b] = RawRows<T>::load(rx, n < r.dn ? static_cast<uint32_t>((l15 * r.ldx + n) * sizeof(T)) : kOutside);
-        }
-      }
-    }
     if constexpr (MODE == kAgg) issue(REV ? c - 1 : c + 1, it + 1 < nch);
     const float wc = sF[M::wc + buf];
 
     f32x4_t Y[NB][NIB];
     if constexpr (MODE != kAgg) {
+      // X where this wavefront's part of the output is
+      typename RawRows<T>::type xv[kDg ? NB : 1][kDg ? NIB : 1];
+      if constexpr (kDg) {
+#pragma unroll
+        for (int b = 0; b < NIB; b++) {
+          const __amdgpu_buffer_rsrc_t rx = rows_rsrc(Xp + (tb + 16 * b) * r.ldx, r.ldx, nv - 16 * b, r.dn, sizeof(T));
+#pragma unroll
+          for (int nb = 0; nb < NB; nb++) {
+            const int n = n0 + 16 * nb + 4 * g;
+            xv[nb][b] = RawRows<T>::load(rx, n < r.dn ? static_cast<uint32_t>((l15 * r.ldx + n) * sizeof(T)) : kOutside);
+          }
+        }
+      }
       // decayed scores of this wavefront's row block i, transposed: lane l
       // holds row i = l % 16 and four consecutive columns j
       const int ib = wave % NIB;
@@ -474,45 +549,66 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
       if constexpr (kBf) {
         if ((ib & 1) == (REV ? 1 : 0)) store4(sP + at_p<T>(i, 16 * (REV ? ib - 1 : ib + 1) + 4 * g), f32x4_t{0.f, 0.f, 0.f, 0.f});
       }
+      // operands of a block, read one block ahead
+      constexpr int KF = DM * (int)sizeof(T) / 64, VF = MODE == kOutFwdDg ? DN * (int)sizeof(T) / 64 : 1;
+      u32x4_t qf[KF], kf[KF], vf[VF];
+      auto read_block = [&](int jb) {
+        const T* const k0 = sK + at<T, DM>(l15, C::EPV * g) + 16 * jb * M::PM;
+#pragma unroll
+        for (int b = 0; b < KF; b++) kf[b] = *reinterpret_cast<const u32x4_t*>(k0 + 4 * C::EPV * b);
+        if constexpr (MODE == kOutFwdDg) {
+          const T* const v0 = sV + at<T, DN>(l15, C::EPV * g) + 16 * jb * M::PN;
+#pragma unroll
+          for (int b = 0; b < VF; b++) vf[b] = *reinterpret_cast<const u32x4_t*>(v0 + 4 * C::EPV * b);
+        }
+      };
+      const T* const q0 = sQ + at<T, DM>(l15, C::EPV * g) + 16 * ib * M::PM;
+#pragma unroll
+      for (int b = 0; b < KF; b++) qf[b] = *reinterpret_cast<const u32x4_t*>(q0 + 4 * C::EPV * b);
+      // blocks the mask leaves: up to ib, or from it (with JW > 1, each wavefront every JW-th)
+      const int jb_end = REV ? NIB : ib + 1;
+      int jb_first = wave / NIB;
+      if (REV)
+        while (jb_first < ib) jb_first += JW;
+      if constexpr (MODE == kOutFwdDg) {
+        for (int jb = jb_first; jb < NIB; jb += JW)
+          if (jb >= jb_end && l15 < 4) sCol[ib * CH + 16 * jb + 4 * g + l15] = 0.0f;
+      }
+      if (jb_first < jb_end) read_block(jb_first);
 #pragma unroll 1
-      for (int jb = wave / NIB; jb < NIB; jb += JW) {
-        if (REV ? jb < ib : jb > ib) {
-          if constexpr (MODE == kOutFwdDg) {
-            if (l15 < 4) sCol[ib * CH + 16 * jb + 4 * g + l15] = 0.0f;
-          }
-        } else {
+      for (int jb = jb_first; jb < jb_end; jb += JW) {
+        {
           f32x4_t p;
           float colsum[4];
           f32x4_t acc{0.f, 0.f, 0.f, 0.f};
           f32x4_t acx{0.f, 0.f, 0.f, 0.f};
-          const int rj = 16 * jb + l15;
           if constexpr (kBf) {
 #pragma unroll
-            for (int kb = 0; kb < DM / 32; kb++)
-              acc = mfma_bf16(load8(sK + at<T, DM>(rj, 32 * kb + 8 * g)), load8(sQ + at<T, DM>(i, 32 * kb + 8 * g)), acc);
+            for (int b = 0; b < KF; b++)
+              acc = mfma_bf16(__builtin_bit_cast(bf16x8_t, kf[b]), __builtin_bit_cast(bf16x8_t, qf[b]), acc);
+            if constexpr (MODE == kOutFwdDg) {
+              // the other pair's scores, X_i . V_j
+#pragma unroll
+              for (int b = 0; b < VF; b++)
+                acx = mfma_bf16(__builtin_bit_cast(bf16x8_t, vf[b]), __builtin_bit_cast(bf16x8_t, xf[b]), acx);
+            }
           } else {
 #pragma unroll
-            for (int b = 0; b < DM / 16; b++) {
-              const f32x4_t ka = load4(sK + at<T, DM>(rj, 16 * b + 4 * g)), qa = load4(sQ + at<T, DM>(i, 16 * b + 4 * g));
+            for (int b = 0; b < KF; b++) {
+              const f32x4_t ka = __builtin_bit_cast(f32x4_t, kf[b]), qa = __builtin_bit_cast(f32x4_t, qf[b]);
 #pragma unroll
               for (int e = 0; e < 4; e++) acc = mfma_f32(ka[e], qa[e], acc);
             }
-          }
-          if constexpr (MODE == kOutFwdDg) {
-            // the other pair's scores, X_i . V_j
-            if constexpr (kBf) {
+            if constexpr (MODE == kOutFwdDg) {
 #pragma unroll
-              for (int kb = 0; kb < DN / 32; kb++)
-                acx = mfma_bf16(load8(sV + at<T, DN>(rj, 32 * kb + 8 * g)), load8(sX + at<T, DN>(i, 32 * kb + 8 * g)), acx);
-            } else {
-#pragma unroll
-              for (int b = 0; b < DN / 16; b++) {
-                const f32x4_t va = load4(sV + at<T, DN>(rj, 16 * b + 4 * g)), xa = load4(sX + at<T, DN>(i, 16 * b + 4 * g));
+              for (int b = 0; b < VF; b++) {
+                const f32x4_t va = __builtin_bit_cast(f32x4_t, vf[b]), xa = __builtin_bit_cast(f32x4_t, xf[b]);
 #pragma unroll
                 for (int e = 0; e < 4; e++) acx = mfma_f32(va[e], xa[e], acx);
               }
             }
           }
+          if (jb + JW < jb_end) read_block(jb + JW);
           const int j0 = 16 * jb + 4 * g;
           const f32x4_t ghj = load4(gh + j0), glj = load4(gl + j0);
 #pragma unroll
@@ -546,7 +642,8 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 
       if constexpr (kDg) keep_state(c);
       // the next chunk's loads: after the scores, whose registers they take
-      issue(REV ? c - 1 : c + 1, it + 1 < nch);
+      // (with the decay gradient's operands, after the output, which takes more)
+      if constexpr (!kDg) issue(REV ? c - 1 : c + 1, it + 1 < nch);
 
       // the state's part, transposed: rows n of this wavefront, columns i
 #pragma unroll
@@ -556,13 +653,11 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
       if constexpr (kBf) {
 #pragma unroll
         for (int kb = 0; kb < MB / 2; kb++) {
-          __builtin_amdgcn_sched_barrier(0);
           bf16x8_t qf[NIB];
 #pragma unroll
           for (int b = 0; b < NIB; b++) {
-            const int q0 = at<T, DM>(16 * b + l15, 32 * kb + 4 * g), q1 = at<T, DM>(16 * b + l15, 32 * kb + 16 + 4 * g);
-            qf[b] = __builtin_bit_cast(bf16x8_t, (Pair64{*reinterpret_cast<const uint2*>(sQ + q0),
-                                                         *reinterpret_cast<const uint2*>(sQ + q1)}));
+            const int q = at<T, DM>(16 * b + l15, 4 * g) + 32 * kb;
+            qf[b] = load44(sQ + q, sQ + q + 16);
           }
 #pragma unroll
           for (int nb = 0; nb < NB; nb++) {
@@ -597,12 +692,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
           Y[nb][b] = Y[nb][b] * w;
-          if constexpr (MODE == kOutFwdDg) {
-            const f32x4_t x = load4(sX + at<T, DN>(16 * b + l15, n0 + 16 * nb + 4 * g));
-#pragma unroll
-            for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
-          }
-          if constexpr (MODE == kOutRevDg) {
+          if constexpr (kDg) {
             const f32x4_t x = RawRows<T>::f32(xv[nb][b]);
 #pragma unroll
             for (int e = 0; e < 4; e++) dot = fmaf(x[e], Y[nb][b][e], dot);
@@ -614,9 +704,13 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
         }
       }
     }
-    if constexpr (MODE != kAgg) lds_barrier();  // scores and partial sums are in LDS; gh, gl, wq are free
-    issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
-    if (wave == kDecayWave && it + 1 < nch) decays(buf ^ 1);
+    // while the other wavefronts have scores left
+    if (wave == kDecayWave) {
+      if (it + 1 < nch) decays(buf ^ 1);
+      if constexpr (kDg)
+        if (it > 0) token_sums(REV ? c + 1 : c - 1, buf ^ 1);
+    }
+    if constexpr (MODE != kAgg) lds_barrier();  // scores and partial sums are in LDS
 
     __builtin_amdgcn_sched_barrier(0);
     // V of this wavefront's columns, tokens along the lane's elements
@@ -626,7 +720,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
       for (int kb = 0; kb < CH / 32; kb++)
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
-          vf[kb][nb] = read_tr<DN>(sV, 32 * kb + 8 * g, n0 + 16 * nb, l15);
+          vf[kb][nb] = read_tr<DN>(sV, 32 * kb, n0 + 16 * nb, lane_now);
         }
       if constexpr (MODE != kAgg) {
 #pragma unroll
@@ -634,10 +728,15 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 #pragma unroll
           for (int kb = 0; kb < CH / 32; kb++)
             if (REV ? 2 * kb + 1 >= b : 2 * kb <= b) {
-              const bf16x8_t pf = load8(sP + at_p<T>(16 * b + l15, 32 * kb + 8 * g));
+              const bf16x8_t pf = load44(sP + at_p<T>(16 * b + l15, 32 * kb + 4 * g), sP + at_p<T>(16 * b + l15, 32 * kb + 16 + 4 * g));
 #pragma unroll
               for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
             }
+        if constexpr (kDg) {
+          __builtin_amdgcn_sched_barrier(0);
+          issue(REV ? c - 1 : c + 1, it + 1 < nch);
+          issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
+        }
         put(tb, nv, Y);
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -648,24 +747,23 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
         for (int nb = 0; nb < NB; nb++) S[mb][nb] = S[mb][nb] * wc;
 #pragma unroll
       for (int kb = 0; kb < CH / 32; kb++) {
-        __builtin_amdgcn_sched_barrier(0);
-        const f32x4_t w0 = load4(wk + 32 * kb + 8 * g), w1 = load4(wk + 32 * kb + 8 * g + 4);
-        bf16x8_t vw[NB][kParts];
+        const f32x4_t w0 = load4(wk + 32 * kb + 4 * g), w1 = load4(wk + 32 * kb + 16 + 4 * g);
+        bf16x8_t vw[NB][PARTS];
 #pragma unroll
         for (int nb = 0; nb < NB; nb++) {
           float u[8];
 #pragma unroll
-          for (int e = 0; e < 8; e++) u[e] = static_cast<float>(vf[kb][nb][e]) * (e < 4 ? w0[e % 4] : w1[e % 4]);
+          for (int e = 0; e < 8; e++) u[e] = widen(vf[kb][nb], e) * (e < 4 ? w0[e % 4] : w1[e % 4]);
 #pragma unroll
-          for (int part = 0; part < kParts; part++) vw[nb][part] = take_part(u, part + 1 < kParts);
+          for (int part = 0; part < PARTS; part++) vw[nb][part] = take_part(u, part + 1 < PARTS);
         }
 #pragma unroll
         for (int mb = 0; mb < MB; mb++) {
-          const bf16x8_t kf = read_tr<DM>(sK, 32 * kb + 8 * g, 16 * mb, l15);
+          const bf16x8_t kf = read_tr<DM>(sK, 32 * kb, 16 * mb, lane_now);
 #pragma unroll
           for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-            for (int part = 0; part < kParts; part++) S[mb][nb] = mfma_bf16(kf, vw[nb][part], S[mb][nb]);
+            for (int part = 0; part < PARTS; part++) S[mb][nb] = mfma_bf16(kf, vw[nb][part], S[mb][nb]);
         }
       }
     } else {
@@ -702,35 +800,19 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
             for (int nb = 0; nb < NB; nb++) S[mb][nb] = mfma_f32(kf, vf[e][nb] * w[e], S[mb][nb]);
           }
       }
+      if constexpr (kDg) {
+        issue(REV ? c - 1 : c + 1, it + 1 < nch);
+        issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
+      }
       if constexpr (MODE != kAgg) put(tb, nv, Y);
     }
     if constexpr (MODE == kAgg) decay_seg *= wc;
 
-    if constexpr (MODE != kAgg) {
-      // one lane per token: the decay gradient's sums inside the chunk
-      if constexpr (kDg) {
-        if (wave == kDecayWave) {
-          double x = 0.0;
-          if (lane < CH) {
-            for (int w = 0; w < 4; w++) x += sRint[w * CH + lane];
-            if constexpr (MODE == kOutFwdDg) {
-              for (int w = 0; w < JW; w++) x += sRow[w * CH + lane];
-              for (int w = 0; w < NIB; w++) x -= sCol[w * CH + lane];
-            }
-          }
-          if constexpr (MODE == kOutFwdDg) {
-            // sums over i >= t
-#pragma unroll
-            for (int d = 1; d < CH; d <<= 1) {
-              const double u = __shfl_down(x, d, 64);
-              if (lane + d < CH) x += u;
-            }
-          } else {
-            x = prefix_sum(x);  // sums over j <= t
-          }
-          if (lane < nv) r.tok[static_cast<int64_t>(h) * a.sq.T + tb + lane] = static_cast<float>(x);
-        }
-      }
+  }
+  if constexpr (kDg) {
+    if (nch > 0) {
+      lds_barrier();
+      if (wave == kDecayWave) token_sums(REV ? 0 : nch - 1, (nch - 1) & 1);
     }
   }
 
@@ -743,15 +825,15 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     s_out = r.s_end + (static_cast<int64_t>(sg.seq) * a.Hv + h) * a.dkdv;
   }
   if (s_out) {
+    const __amdgpu_buffer_rsrc_t rs = state_rsrc(s_out);
 #pragma unroll
     for (int mb = 0; mb < MB; mb++)
 #pragma unroll
-      for (int nb = 0; nb < NB; nb++) {
-        const int m = 16 * mb + 4 * g, n = n0 + 16 * nb + l15;
-        if (m < r.dm && n < r.dn)
+      for (int nb = 0; nb < NB; nb++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) s_out[(m + e) * r.sm + n * r.sn] = S[mb][nb][e];
-      }
+        for (int e = 0; e < 4; e++)
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[mb][nb][e]), rs,
+                                                state_off(mb, nb) + static_cast<uint32_t>(e * r.sm) * 4u, 0, 0);
   }
 }
 
@@ -773,28 +855,37 @@ __device__ __forceinline__ Work work_of(const Args& a, int nz) {
   w.any = u < a.units;
   w.slot = u / per_slot;
   w.h = static_cast<int>(u % per_slot * a.unit_heads + k / nz);
-  w.z = static_cast<int>(k % nz);
+  w.z = a.run_of[k % nz];
   return w;
+}
+
+// Workgroups that share a CU: as many as the state's registers leave room
+// for (the LDS does too).
+constexpr int wgs_per_cu(int dk, int dv, int kind) {
+  const int n = dk * dv > 64 * 64 ? 2 : 3;
+  return kind == kAggregate ? n + 1 : n;
 }
 
 // Kinds: kGrad... with PT the type of dq and dk, float where the value heads
 // of a key head are summed afterwards.
 template <class T, class PT, int DK, int DV, int KIND>
-__global__ __launch_bounds__(kThreads, 2) void k_linattn(Args a) {
+__global__ __launch_bounds__(kThreads, wgs_per_cu(DK, DV, KIND)) void k_linattn(Args a) {
   extern __shared__ __attribute__((aligned(16))) char smem_la[];
   const Work w = work_of(a, a.nz);
   if (!w.any) return;
-  const Run& r = a.run[w.z];
+  constexpr int P2 = 2;
   if constexpr (KIND == kForward) {
-    run<T, T, DK, DV, false, kOut>(a, r, w.slot, w.h, smem_la);
+    run<T, T, DK, DV, false, kOut, P2>(a, a.run[0], w.slot, w.h, smem_la);
+  } else if constexpr (KIND == kForwardState) {
+    run<T, T, DK, DV, false, kOut, kParts>(a, a.run[0], w.slot, w.h, smem_la);
   } else if constexpr (KIND == kAggregate) {
-    if (w.z == 0) run<T, T, DK, DV, false, kAgg>(a, r, w.slot, w.h, smem_la);
-    else run<T, T, DK, DV, true, kAgg>(a, r, w.slot, w.h, smem_la);
+    if (w.z == 0) run<T, T, DK, DV, false, kAgg, kParts>(a, a.run[0], w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kAgg, kParts>(a, a.run[1], w.slot, w.h, smem_la);
   } else {
     constexpr bool dg = KIND == kGradDecay;
-    if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut>(a, r, w.slot, w.h, smem_la);
-    else if (w.z == 1) run<T, PT, DV, DK, true, dg ? kOutRevDg : kOut>(a, r, w.slot, w.h, smem_la);
-    else run<T, T, DK, DV, true, kOut>(a, r, w.slot, w.h, smem_la);
+    if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut, dg ? kParts : P2>(a, a.run[0], w.slot, w.h, smem_la);
+    else if (w.z == 1) run<T, PT, DV, DK, true, dg ? kOutRevDg : kOut, kParts>(a, a.run[1], w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kOut, P2>(a, a.run[2], w.slot, w.h, smem_la);
   }
 }
 
@@ -802,7 +893,7 @@ constexpr int max2(int a, int b) { return a > b ? a : b; }
 
 template <class T, int DK, int DV, int KIND>
 constexpr int lds_bytes() {
-  if (KIND == kForward) return Lds<T, DK, DV, kOut>::bytes;
+  if (KIND == kForward || KIND == kForwardState) return Lds<T, DK, DV, kOut>::bytes;
   if (KIND == kAggregate) return Lds<T, DK, DV, kAgg>::bytes;
   if (KIND == kGradDecay) return max2(Lds<T, DV, DK, kOutFwdDg>::bytes, Lds<T, DK, DV, kOut>::bytes);
   return max2(Lds<T, DV, DK, kOut>::bytes, Lds<T, DK, DV, kOut>::bytes);
@@ -826,6 +917,7 @@ hipError_t launch_one(const Args& a, hipStream_t st) {
 template <class T, int DK, int DV>
 hipError_t launch_kind(Kernel k, const Args& a, hipStream_t st) {
   if (k == kForward) return launch_one<T, T, DK, DV, kForward>(a, st);
+  if (k == kForwardState) return launch_one<T, T, DK, DV, kForwardState>(a, st);
   if (k == kAggregate) return launch_one<T, T, DK, DV, kAggregate>(a, st);
   if (a.sum_heads)
     return k == kGradDecay ? launch_one<T, float, DK, DV, kGradDecay>(a, st)
