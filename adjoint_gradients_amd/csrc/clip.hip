@@ -8,6 +8,10 @@
 // scaling walks the tensors from the end, so that what the first pass read
 // last, and the caches still hold, is read first.
 //
+// Few elements (kSmall, in a few tensors) are one workgroup's work: it adds
+// and then scales in one launch, which costs less than the second launch
+// would.
+//
 // The tensor table travels in the kernel arguments, kTable tensors a launch:
 // nothing is copied to the device, and a captured launch keeps its own.
 #include <math.h>
@@ -23,6 +27,8 @@ namespace {
 
 constexpr int kTable = 96;             // tensors a launch (3 KB of arguments)
 constexpr int kBlock = 8192;           // elements a workgroup takes at a time
+constexpr int64_t kSmall = 32768;      // elements of the one-launch form,
+constexpr int kSmallCount = 16;        // which walks its tensors one by one
 constexpr int64_t kMaxWgs = 1024;      // per launch: also its partial sums
 constexpr int32_t kMaxTensors = 65536;
 constexpr int64_t kMaxElems = int64_t(1) << 40;
@@ -123,6 +129,64 @@ __global__ __launch_bounds__(256) void k_square_sums(Table t, double* __restrict
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
+// The factor of the scaling; 1 where nothing is clipped.
+__device__ __forceinline__ float clip_factor(double total, float max_norm) {
+  const bool clip = total > static_cast<double>(max_norm) && isfinite(total);
+  return clip ? static_cast<float>(static_cast<double>(max_norm) / total) : 1.0f;
+}
+
+// Both passes over a table of at most kSmall elements, one workgroup.
+template <class T>
+__global__ __launch_bounds__(1024) void k_clip_small(Table t, float max_norm, int scale, float* __restrict__ norm) {
+  __shared__ double red[16];
+  constexpr int N = Vec<T>::N;
+  double s = 0.0;
+  for (int i = 0; i < t.count; i++) {
+    const T* const src = static_cast<const T*>(t.in[i]);
+    const int n = static_cast<int>(t.n[i]), nv = n / N;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < nv; e += 1024) {
+      float f[N];
+      Vec<T>::get(reinterpret_cast<const uint4*>(src)[e], f);
+#pragma unroll
+      for (int k = 0; k < N; k++) s = fma(static_cast<double>(f[k]), static_cast<double>(f[k]), s);
+    }
+    if (static_cast<int>(threadIdx.x) < n - nv * N) {
+      const double v = load_io(src + nv * N + threadIdx.x);
+      s = fma(v, v, s);
+    }
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) s += __shfl_xor(s, d, 64);
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < 16; w++) s += red[w];
+  const double total = sqrt(s);
+  if (threadIdx.x == 0) *norm = static_cast<float>(total);
+  if (!scale) return;
+  const float c = clip_factor(total, max_norm);
+  for (int i = 0; i < t.count; i++) {
+    const T* const src = static_cast<const T*>(t.in[i]);
+    T* const dst = static_cast<T*>(t.out[i]);
+    if (c == 1.0f && dst == src) continue;
+    const int n = static_cast<int>(t.n[i]), nv = n / N;
+#pragma unroll 2
+    for (int e = threadIdx.x; e < nv; e += 1024) {
+      float f[N];
+      Vec<T>::get(reinterpret_cast<const uint4*>(src)[e], f);
+#pragma unroll
+      for (int k = 0; k < N; k++) f[k] = c == 1.0f ? f[k] : f[k] * c;
+      reinterpret_cast<uint4*>(dst)[e] = Vec<T>::put(f);
+    }
+    if (static_cast<int>(threadIdx.x) < n - nv * N) {
+      const float f = load_io(src + nv * N + threadIdx.x);
+      store_io(dst + nv * N + threadIdx.x, c == 1.0f ? f : f * c);
+    }
+  }
+}
+
 template <class T>
 __global__ __launch_bounds__(256) void k_clip_scale(Table t, const double* __restrict__ part, int nparts,
                                                    float max_norm, int scale, float* __restrict__ norm) {
@@ -133,8 +197,8 @@ __global__ __launch_bounds__(256) void k_clip_scale(Table t, const double* __res
   const double total = sqrt(wg_sum(s, red));
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
   if (!scale) return;
-  const bool clip = total > static_cast<double>(max_norm) && isfinite(total);
-  const float c = clip ? static_cast<float>(static_cast<double>(max_norm) / total) : 1.0f;
+  const float c = clip_factor(total, max_norm);
+  const bool clip = c != 1.0f;
   for (int64_t i = blockIdx.x; i < t.blocks; i += gridDim.x) {
     const Piece p = piece_of(t, t.blocks - 1 - i);
     const T* const src = static_cast<const T*>(t.in[p.tensor]) + p.e0;
@@ -191,6 +255,12 @@ Table table_of(int32_t first, int32_t count, const void* const* in, void* const*
 template <class T>
 hipError_t run_clip(int32_t count, const void* const* in, void* const* out, const int64_t* n, float max_norm,
                     float* norm, double* part, hipStream_t st) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; i++) total += n[i];
+  if (count <= kSmallCount && total <= kSmall) {
+    k_clip_small<T><<<1, 1024, 0, st>>>(table_of(0, count, in, out, n), max_norm, out ? 1 : 0, norm);
+    return hipGetLastError();
+  }
   int nparts = 0;
   for (int32_t i = 0; i < count; i += kTable) {
     const Table t = table_of(i, count, in, out, n);

@@ -88,9 +88,14 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
 
 // out[t][hk][c] = sum over the heads of hk's group, in order, for the rows the
 // sequences cover.  One thread per four channels.
+struct GroupArgs {
+  const float* part;  // [T][Hv][d]
+  void* out;          // [T][Hk][d] in the io type
+};
+
 template <class T>
-__global__ __launch_bounds__(256) void k_la_group_sum(Seqs sq, int32_t Hk, int32_t G, int32_t d,
-                                                     const float* __restrict__ part, T* __restrict__ out) {
+__device__ __forceinline__ void group_sum(const Seqs& sq, int32_t Hk, int32_t G, int32_t d, const GroupArgs& a,
+                                          int64_t wg, int64_t wgs) {
   int64_t t0 = 0, t1 = sq.T;
   if (sq.start) {
     t0 = sq.start[0];
@@ -100,11 +105,11 @@ __global__ __launch_bounds__(256) void k_la_group_sum(Seqs sq, int32_t Hk, int32
   }
   const int d4 = d / 4;
   const int64_t n = t1 * Hk * d4;
-  for (int64_t i = t0 * Hk * d4 + static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
+  T* const out = static_cast<T*>(a.out);
+  for (int64_t i = t0 * Hk * d4 + wg * 256 + threadIdx.x; i < n; i += wgs * 256) {
     const int64_t th = i / d4;
     const int c = static_cast<int>(i % d4) * 4;
-    const float* p = part + th * G * d + c;
+    const float* p = a.part + th * G * d + c;
     float4 s = *reinterpret_cast<const float4*>(p);
     for (int g = 1; g < G; g++) {
       const float4 v = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(g) * d);
@@ -140,10 +145,8 @@ __device__ __forceinline__ double wg_sum(double v, double* red) {
   return (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-__global__ __launch_bounds__(256) void k_la_decay_grad(DecayArgs a) {
+__device__ __forceinline__ void decay_grad(const DecayArgs& a, uint32_t slot, int h) {
   __shared__ double red[4], xs[kAnchor], all_i[kAnchor], all_j[kAnchor];
-  const uint32_t slot = blockIdx.x;
-  const int h = blockIdx.y;
   Segment sg;
   const bool have = find_segment(a.sq, slot, a.ch, &sg);
   double sum = 0.0;
@@ -199,6 +202,27 @@ __global__ __launch_bounds__(256) void k_la_decay_grad(DecayArgs a) {
     sum = wg_sum(sum, red);
     if (threadIdx.x == 0) a.dg_seg[static_cast<int64_t>(slot) * a.Hv + h] = sum;
   }
+}
+
+// What follows the runs of the gradient, in one launch: first the workgroups
+// of the decay gradient (decay_wgs of them), then those of the sums of dq and
+// of dk over shared heads (sum_wgs each).
+struct FinishArgs {
+  DecayArgs decay;
+  GroupArgs group[2];
+  int32_t Hk, dk;
+  uint32_t decay_wgs, sum_wgs;
+};
+
+template <class T>
+__global__ __launch_bounds__(256) void k_la_finish(FinishArgs a) {
+  const uint32_t b = blockIdx.x;
+  if (b < a.decay_wgs) {
+    decay_grad(a.decay, b / a.decay.Hv, static_cast<int>(b % a.decay.Hv));
+    return;
+  }
+  const uint32_t k = b - a.decay_wgs;
+  group_sum<T>(a.decay.sq, a.Hk, a.decay.Hv / a.Hk, a.dk, a.group[k / a.sum_wgs], k % a.sum_wgs, a.sum_wgs);
 }
 
 // out[h] = sum over the segments, in a fixed order, in 64 bits.
@@ -305,6 +329,7 @@ using abi::good;
 using abi::good_or_null;
 
 constexpr int32_t kMaxHeads = 4096, kMaxSeqs = 65535;
+constexpr int64_t kMaxSeqHeads = int64_t(1) << 22;  // three runs of them are a grid's limit of 2^32 lanes
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // a chunk's rows stay within 32-bit byte offsets
 constexpr int64_t kMaxStepRows = int64_t(1) << 22;
 
@@ -317,6 +342,7 @@ ssm_status check_dims(const ssm_linattn_dims* d) {
   if (d->io != SSM_F32 && d->io != SSM_BF16) return SSM_ERR_UNSUPPORTED;
   if (d->dk % 8 || d->dv % 8 || d->dk > 128 || d->dv > 128) return SSM_ERR_UNSUPPORTED;
   if (d->Hv > kMaxHeads || d->S > kMaxSeqs || d->T > INT32_MAX) return SSM_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(d->S) * d->Hv > kMaxSeqHeads) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -519,16 +545,6 @@ hipError_t run_forward(const ssm_linattn_dims* d, const ssm_linattn_in* in, void
   return launch(hT ? kForwardState : kForward, d, a, st);
 }
 
-hipError_t group_sum(const ssm_linattn_dims* d, const Seqs& sq, const float* part, void* out, hipStream_t st) {
-  const int64_t n = d->T * d->Hk * (d->dk / 4);
-  const int64_t wgs = (n + 255) / 256;
-  const unsigned grid = static_cast<unsigned>(wgs < 4096 ? wgs : 4096);
-  const int32_t G = d->Hv / d->Hk;
-  if (d->io == SSM_BF16) k_la_group_sum<<<grid, 256, 0, st>>>(sq, d->Hk, G, d->dk, part, static_cast<bf16_t*>(out));
-  else k_la_group_sum<<<grid, 256, 0, st>>>(sq, d->Hk, G, d->dk, part, static_cast<float*>(out));
-  return hipGetLastError();
-}
-
 hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const void* dy, int64_t lddy,
                     const float* dhT, const ssm_linattn_grads* g, void* ws, hipStream_t st) {
   const Plan p = make_plan(d, g, in->seq_start != nullptr);
@@ -578,19 +594,34 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   a.run[1] = need_k ? rk : Run{};
   a.run[2] = g->dv ? rv : Run{};
   if ((e = launch(p.dg ? kGradDecay : kGradPlain, d, a, st)) != hipSuccess) return e;
+  FinishArgs f{};
+  f.decay.sq = a.sq;
+  f.decay.Hv = d->Hv;
+  f.Hk = d->Hk;
+  f.dk = d->dk;
   if (p.dg) {
-    const DecayArgs da{a.sq, d->Hv, chunk_tokens(d->io == SSM_BF16),
-                       static_cast<int32_t>(state_floats(d->dk, d->dv) / 4), in->log_decay, a.ld_decay, w.tok[0],
-                       w.tok[1], w.anchors[0], w.anchors[1], d->decay_tokens ? g->dlog_decay : nullptr, w.dg_seg};
-    k_la_decay_grad<<<dim3(static_cast<unsigned>(p.slots), static_cast<unsigned>(d->Hv)), 256, 0, st>>>(da);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (!d->decay_tokens) {
-      k_la_decay_sum<<<static_cast<unsigned>(d->Hv), 256, 0, st>>>(p.slots, d->Hv, w.dg_seg, g->dlog_decay);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    f.decay = DecayArgs{a.sq, d->Hv, chunk_tokens(d->io == SSM_BF16),
+                        static_cast<int32_t>(state_floats(d->dk, d->dv) / 4), in->log_decay, a.ld_decay, w.tok[0],
+                        w.tok[1], w.anchors[0], w.anchors[1], d->decay_tokens ? g->dlog_decay : nullptr, w.dg_seg};
+    f.decay_wgs = static_cast<uint32_t>(p.slots * d->Hv);
   }
-  if (w.part[0] && (e = group_sum(d, a.sq, w.part[0], g->dq, st)) != hipSuccess) return e;
-  if (w.part[1] && (e = group_sum(d, a.sq, w.part[1], g->dk, st)) != hipSuccess) return e;
+  uint32_t sums = 0;
+  for (int i = 0; i < 2; i++)
+    if (w.part[i]) f.group[sums++] = GroupArgs{w.part[i], i == 0 ? g->dq : g->dk};
+  if (sums) {
+    const int64_t wgs = (d->T * d->Hk * (d->dk / 4) + 255) / 256;
+    f.sum_wgs = static_cast<uint32_t>(wgs < 2048 ? wgs : 2048);
+  }
+  const uint32_t grid = f.decay_wgs + sums * f.sum_wgs;
+  if (grid) {
+    if (d->io == SSM_BF16) k_la_finish<bf16_t><<<grid, 256, 0, st>>>(f);
+    else k_la_finish<float><<<grid, 256, 0, st>>>(f);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (w.dg_seg) {
+    k_la_decay_sum<<<static_cast<unsigned>(d->Hv), 256, 0, st>>>(p.slots, d->Hv, w.dg_seg, g->dlog_decay);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   return hipSuccess;
 }
 

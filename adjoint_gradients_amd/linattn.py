@@ -122,35 +122,65 @@ def _rows(t, name: str, lead, device, dtype, heads=None):
     return hd, ld
 
 
+# What _setup found for contiguous inputs of these shapes and types: it goes by
+# them alone, and checking a small call again costs as much as launching it.
+_plans: dict = {}
+
+
 def _setup(q, k, v, log_decay, scale, seq_start, device, step=False):
     """Checks the inputs; returns (dims, leading shape, v's heads, LinattnIn)."""
+    starts, S = None, 0
+    if seq_start is not None:
+        S = seq_start.numel() - 1 if isinstance(seq_start, torch.Tensor) else 0
+        if S < 1:
+            _bad("seq_start: expected an int32 tensor of at least two offsets")
+        starts = _dense(seq_start, "seq_start", (S + 1,), device, torch.int32)
+    if type(scale) is not float:
+        scale = float(scale)
+    io = q.dtype
+    key = None
+    try:
+        if (k.get_device() == v.get_device() == log_decay.get_device() == device and k.dtype is io and v.dtype is io
+                and log_decay.dtype is torch.float32 and q.is_contiguous() and k.is_contiguous()
+                and v.is_contiguous() and log_decay.is_contiguous()):
+            key = (q.shape, k.shape, v.shape, log_decay.shape, io, scale, S, step)
+    except AttributeError:
+        pass  # not a tensor: refused below by name
+    plan = _plans.get(key) if key is not None else None
+    if plan is None:
+        plan = _check_inputs(q, k, v, log_decay, scale, S, device, step)
+        if key is not None:
+            if len(_plans) >= 256:
+                _plans.clear()
+            _plans[key] = plan
+    dims, lead, hv, ldq, ldk, ldv = plan
+    return dims, lead, hv, LinattnIn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, log_decay.data_ptr(),
+                                     starts, None)
+
+
+def _check_inputs(q, k, v, log_decay, scale, packed, device, step):
     io = q.dtype
     if io not in _IO:
         _bad(f"q: dtype {io}, expected bfloat16 or float32")
     nd = q.dim()
     if nd != 3 and (nd != 4 or step):
         _bad(f"q: {nd} dimensions")
+    if packed and nd != 3:
+        _bad("seq_start goes with packed tokens [T, H, d]")
     lead = q.shape[:-2]
     hk, ldq = _rows(q, "q", lead, device, io)
     _, ldk = _rows(k, "k", lead, device, io, hk)
     hv, ldv = _rows(v, "v", lead, device, io)
-    T, S, starts = q.shape[0], 1, None
+    T, S = q.shape[0], packed or 1
     if nd == 4:
         S, T = T, T * q.shape[1]
     if T < 1 or hk[0] < 1 or hv[0] < 1:
         _bad("no tokens or no heads")
-    if seq_start is not None:
-        if nd != 3:
-            _bad("seq_start goes with packed tokens [T, H, d]")
-        S = seq_start.numel() - 1 if isinstance(seq_start, torch.Tensor) else 0
-        if S < 1:
-            _bad("seq_start: expected an int32 tensor of at least two offsets")
-        starts = _dense(seq_start, "seq_start", (S + 1,), device, torch.int32)
     _gpu(log_decay, "log_decay", device, torch.float32)
     tokens = log_decay.dim() != 1
-    g = _dense(log_decay, "log_decay", lead + hv[:1] if tokens else hv[:1], device, torch.float32)
+    _dense(log_decay, "log_decay", lead + hv[:1] if tokens else hv[:1], device, torch.float32)
     dims = LinattnDims(T, S, hk[0], hv[0], hk[1], hv[1], _IO[io], 1 if tokens else 0, scale)
-    return dims, lead, hv, LinattnIn(q.data_ptr(), k.data_ptr(), v.data_ptr(), ldq, ldk, ldv, g, starts, None)
+    return dims, lead, hv, ldq, ldk, ldv
 
 
 def linattn_workspace_bytes(dims: LinattnDims, grads: LinattnGrads | None = None) -> int:
@@ -187,7 +217,7 @@ def linattn_forward(q, k, v, log_decay, seq_start=None, h0=None, scale=1.0, want
     states = (dims.S, dims.Hv, dims.dk, dims.dv)
     ins.h0 = _dense(h0, "h0", states, device, torch.float32)
     if y is None:
-        y = torch.empty_like(v, memory_format=torch.contiguous_format)
+        y = torch.empty_like(v) if v.is_contiguous() else torch.empty(v.shape, dtype=v.dtype, device=v.device)
         ldy = hv[0] * hv[1]
     else:
         _, ldy = _rows(y, "y", lead, device, q.dtype, hv)
@@ -242,7 +272,7 @@ def linattn_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
         _bad("state is required")
     st = _dense(state, "state", (dims.T, dims.Hv, dims.dk, dims.dv), device, torch.float32)
     if y is None:
-        y = torch.empty_like(v, memory_format=torch.contiguous_format)
+        y = torch.empty_like(v) if v.is_contiguous() else torch.empty(v.shape, dtype=v.dtype, device=v.device)
         ldy = hv[0] * hv[1]
     else:
         _, ldy = _rows(y, "y", lead, device, q.dtype, hv)

@@ -59,12 +59,17 @@ def add_norm(r, y, norm_scale, eps=1e-5, r_out=None, x=None, rinv=None, io=None,
     gp = _dense(norm_scale, "norm_scale", (P,), device, _F32)
     if r_out is None:
         r_out = r if y is None else torch.empty_like(r)
+    elif r_out is not r:
+        _dense(r_out, "r_out", shape, device, _F32)
     if x is None:
-        x = torch.empty_like(r, dtype=dt)
+        x = torch.empty_like(r if y is None else y, dtype=dt)
+    else:
+        _dense(x, "x", shape, device, dt)
     if rinv is None:
         rinv = torch.empty(shape[:-1], dtype=_F32, device=r.device)
-    _check(lib.ssm_add_norm(T, P, _IO[dt], rp, yp, gp, eps, _dense(r_out, "r_out", shape, device, _F32),
-                            _dense(x, "x", shape, device, dt), _dense(rinv, "rinv", shape[:-1], device, _F32),
+    else:
+        _dense(rinv, "rinv", shape[:-1], device, _F32)
+    _check(lib.ssm_add_norm(T, P, _IO[dt], rp, yp, gp, eps, r_out.data_ptr(), x.data_ptr(), rinv.data_ptr(),
                             _raw_stream(device)), "ssm_add_norm")
     return x, r_out, rinv
 

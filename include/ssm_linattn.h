@@ -28,7 +28,7 @@
  * log_decay and its gradient [T][Hv] or [Hv], states [S][Hv][dk][dv], float32.
  *
  * Supported: dk and dv multiples of 8 up to 128, Hk divides Hv, Hv <= 4096,
- * S <= 65535.  log_decay may be -inf (a reset) and positive; a NaN or an
+ * S <= 65535, S * Hv <= 2^22, T < 2^31.  log_decay may be -inf (a reset) and positive; a NaN or an
  * infinity in one token's q, k, v or dy may reach every output of its
  * sequence and head.
  */
