@@ -21,7 +21,7 @@ import ctypes
 
 import torch
 
-from . import SSM_BF16, SSM_F32, SsmError, alloc_workspace, lib
+from . import SSM_BF16, SSM_F32, SsmError, lib
 from . import _check
 
 _P, _VP = ctypes.POINTER, ctypes.c_void_p
@@ -183,6 +183,21 @@ def _check_inputs(q, k, v, log_decay, scale, packed, device, step):
     return dims, lead, hv, ldq, ldk, ldv
 
 
+_sizes: dict = {}
+
+
+def _ws_bytes(dims, grads, wanted) -> int:
+    """linattn_workspace_bytes, remembered by the sizes it follows from."""
+    key = (dims.T, dims.S, dims.Hk, dims.Hv, dims.dk, dims.dv, dims.io, dims.decay_tokens, wanted)
+    n = _sizes.get(key)
+    if n is None:
+        n = linattn_workspace_bytes(dims, grads)
+        if len(_sizes) >= 256:
+            _sizes.clear()
+        _sizes[key] = n
+    return n
+
+
 def linattn_workspace_bytes(dims: LinattnDims, grads: LinattnGrads | None = None) -> int:
     """Workspace of linattn_forward, or of linattn_grad for the outputs set in grads."""
     n = ctypes.c_size_t(0)
@@ -193,7 +208,7 @@ def linattn_workspace_bytes(dims: LinattnDims, grads: LinattnGrads | None = None
 
 def _workspace(ws, nbytes: int, device):
     if ws is None:
-        return alloc_workspace(nbytes, f"cuda:{device}") if nbytes else None
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     _gpu(ws, "workspace", device, torch.uint8)
     if not ws.is_contiguous() or ws.numel() < nbytes:
         raise SsmError(2, f"workspace: {nbytes} contiguous bytes needed")
@@ -224,7 +239,7 @@ def linattn_forward(q, k, v, log_decay, seq_start=None, h0=None, scale=1.0, want
     if hT is None and want_state:
         hT = torch.empty(states, dtype=torch.float32, device=q.device)
     end = _dense(hT, "hT", states, device, torch.float32)
-    w, n = _ws_args(_workspace(ws, linattn_workspace_bytes(dims), device))
+    w, n = _ws_args(_workspace(ws, _ws_bytes(dims, None, None), device))
     _check(lib.ssm_linattn_forward(ctypes.byref(dims), ctypes.byref(ins), y.data_ptr(), ldy, end, w, n,
                                    _raw_stream(device)), "ssm_linattn_forward")
     return y, hT
@@ -253,7 +268,7 @@ def linattn_grad(q, k, v, log_decay, dy, seq_start=None, h0=None, dhT=None, scal
     if grads is None:
         grads = {name: torch.empty(like[name][0], dtype=like[name][1], device=q.device) for name in names}
     g = LinattnGrads(*(_dense(grads.get(name), name, like[name][0], device, like[name][1]) for name in GRADS))
-    w, n = _ws_args(_workspace(ws, linattn_workspace_bytes(dims, g), device))
+    w, n = _ws_args(_workspace(ws, _ws_bytes(dims, g, tuple(name for name in GRADS if grads.get(name) is not None)), device))
     _check(lib.ssm_linattn_grad(ctypes.byref(dims), ctypes.byref(ins), dy.data_ptr(), lddy, end, ctypes.byref(g), w, n,
                                 _raw_stream(device)), "ssm_linattn_grad")
     return grads

@@ -5,7 +5,7 @@ import ctypes
 
 import torch
 
-from . import SsmError, alloc_workspace, lib
+from . import SsmError, lib
 from . import _check
 from .linattn import _IO, _bad, _current_device, _dense, _gpu, _on, _raw_stream, _workspace
 
@@ -108,6 +108,18 @@ def add_norm_grad(r_out, rinv, norm_scale, dx, dr_out=None, dr=None, want_scale=
     return dr, dscale
 
 
+def _addresses(ts, name: str, device, dtype):
+    """The addresses of contiguous tensors of one dtype on one device."""
+    out = []
+    for t in ts:
+        if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype:
+            _gpu(t, name, device, dtype)
+        if not t.is_contiguous():
+            _bad(f"{name}: must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
 def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
     """Scales gradients to a global norm of at most max_norm; returns the norm
     before that, a float32 tensor [1] on the GPU (nothing is synchronised).
@@ -133,18 +145,21 @@ def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
     if not max_norm > 0:
         _bad("max_norm must be positive")
     n = len(ts)
-    pi = [_dense(t, "a gradient", t.shape, device, dt) for t in ts]
+    pi = _addresses(ts, "a gradient", device, dt)
     if out is None:
         po = pi
-        if len(set(pi)) != n and len({p for p, t in zip(pi, ts) if t.numel()}) != sum(1 for t in ts if t.numel()):
-            _bad("clip_grads: a gradient is given twice")
+        if len(set(pi)) != n:
+            used = [p for p, t in zip(pi, ts) if t.numel()]  # empty tensors share the null address
+            if len(set(used)) != len(used):
+                _bad("clip_grads: a gradient is given twice")
     else:
         out = list(out)
         if len(out) != n:
             _bad(f"clip_grads: {len(out)} outputs for {n} gradients")
-        po = [_dense(o, "an output", t.shape, device, dt) for o, t in zip(out, ts)]
-        if None in po:
-            _bad("clip_grads: an output is missing")
+        po = _addresses(out, "an output", device, dt)
+        for o, t in zip(out, ts):
+            if o.shape != t.shape:
+                _bad(f"an output: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
     ptrs, counts = _VP * n, _I64 * n
     ns = counts(*[t.numel() for t in ts])
     nbytes = lib.ssm_clip_grads_workspace_bytes(n, ns)

@@ -1,0 +1,182 @@
+"""The operators at their edges on the GPU: many and long sequences, offsets
+past 32 bits, non-finite tokens, streams, refusals of GPU tensors."""
+import pytest
+import torch
+
+import linattn_ref as ref
+from gpu_util import say
+from test_gpu_linattn import IO, check, device_inputs, spans_of, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def agm():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import adjoint_gradients_amd as agm
+
+    return agm
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_many_sequences(agm, io):
+    """More sequences than any table or wavefront holds, most of them short or empty."""
+    gen = torch.Generator().manual_seed(7)
+    lens = [int(x) for x in torch.randint(0, 9, (150,), generator=gen)] + [0, 301, 0, 65, 1]
+    spans = spans_of(lens, 2)
+    T = spans[-1][1] + 1
+    d = ref.inputs(50, T, 1, 2, 24, 16, io, S=len(lens), states=True)
+    want, ends = ref.forward(d["q"], d["k"], d["v"], d["g"], spans, 0.5, d["h0"])
+    gw, _ = ref.gradient(d["q"], d["k"], d["v"], d["g"], d["dy"], spans, 0.5, d["h0"], d["dhT"])
+    t = device_inputs(d, io)
+    off = starts(spans)
+    y, hT = agm.linattn_forward(t["q"], t["k"], t["v"], t["g"], seq_start=off, h0=t["h0"], scale=0.5, want_state=True)
+    got = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], seq_start=off, h0=t["h0"], dhT=t["dhT"], scale=0.5)
+    check("y", y[2:T - 1].cpu(), want[2:T - 1], io, "many")
+    check("hT", hT.cpu(), ends, io, "many")
+    for n in got:
+        rows = slice(None) if n == "dh0" else slice(2, T - 1)
+        check(n, got[n].cpu()[rows], gw[n][rows], io, "many")
+
+
+def test_offsets_past_32_bits(agm):
+    """v, y and their cotangents of 2.2e9 elements: the last head against the
+    same head computed alone (other segments, so other fp32 carries)."""
+    T, Hv, dk, dv = 133000, 130, 16, 128
+    assert T * Hv * dv > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn(T, 1, dk, generator=gen, device="cuda").bfloat16()
+    k = torch.randn(T, 1, dk, generator=gen, device="cuda").bfloat16()
+    v = torch.empty(T, Hv, dv, dtype=torch.bfloat16, device="cuda")
+    dy = torch.empty_like(v)
+    v.normal_(generator=gen)
+    dy.normal_(generator=gen)
+    g = -torch.rand(T, Hv, generator=gen, device="cuda") * 0.1
+    say("case forward")
+    y, hT = agm.linattn_forward(q, k, v, g, want_state=True)
+    h = Hv - 1
+    one = [v[:, h:].contiguous(), g[:, h:].contiguous(), dy[:, h:].contiguous()]
+    y1, h1 = agm.linattn_forward(q, k, one[0], one[1], want_state=True)
+    # one output rounding each, and the fp32 sums before it
+    assert ref.rms_err(y[:, h:], y1.double().cpu()) <= 2.0 ** -8
+    assert ref.rms_err(hT[:, h:], h1.double().cpu()) <= 2.0 ** -18
+    say("case gradient")
+    a = agm.linattn_grad(q, k, v, g, dy, want=["dv", "dlog_decay"])
+    b = agm.linattn_grad(q, k, one[0], one[1], one[2], want=["dv", "dlog_decay"])
+    assert ref.rms_err(a["dv"][:, h:], b["dv"].double().cpu()) <= 2.0 ** -8
+    assert ref.rms_err(a["dlog_decay"][:, h:], b["dlog_decay"].double().cpu()) <= 2.0 ** -16
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_nonfinite_tokens_stay_in_their_sequence_and_head(agm, io):
+    spans = spans_of([100, 70, 300])
+    T = spans[-1][1]
+    d = ref.inputs(51, T, 2, 2, 32, 32, io, S=3, states=True)
+    t = device_inputs(d, io)
+    clean = agm.linattn_forward(t["q"], t["k"], t["v"], t["g"], seq_start=starts(spans), h0=t["h0"], want_state=True)
+    gclean = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], seq_start=starts(spans), h0=t["h0"], dhT=t["dhT"])
+    for n, bad in (("v", float("inf")), ("k", float("nan")), ("dy", float("nan"))):
+        u = {m: (None if x is None else x.clone()) for m, x in t.items()}
+        u[n][130, 0] = bad  # a token of the second sequence, first head
+        y, hT = agm.linattn_forward(u["q"], u["k"], u["v"], u["g"], seq_start=starts(spans), h0=u["h0"], want_state=True)
+        got = agm.linattn_grad(u["q"], u["k"], u["v"], u["g"], u["dy"], seq_start=starts(spans), h0=u["h0"], dhT=u["dhT"])
+        out = torch.ones(T, dtype=torch.bool, device="cuda")
+        out[100:170] = False
+        assert torch.equal(y[out], clean[0][out]) and torch.equal(y[:, 1], clean[0][:, 1])
+        assert torch.equal(hT[[0, 2]], clean[1][[0, 2]]) and torch.equal(hT[:, 1], clean[1][:, 1])
+        for m in ("dq", "dk", "dv", "dlog_decay"):
+            assert torch.equal(got[m][out], gclean[m][out]) and torch.equal(got[m][:, 1], gclean[m][:, 1]), (n, m)
+
+
+def test_two_streams_at_once(agm):
+    """Calls on two streams with their own workspaces and inputs, interleaved."""
+    ins = [device_inputs(ref.inputs(60 + i, 1500, 2, 2, 64, 64, "bf16", S=1, states=True), "bf16") for i in range(2)]
+
+    def work(t):
+        y, hT = agm.linattn_forward(t["q"], t["k"], t["v"], t["g"], h0=t["h0"], want_state=True)
+        g = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], h0=t["h0"], dhT=t["dhT"])
+        x, r, ri = agm.add_norm(t["h0"].view(-1, 64), None, t["h0"].view(-1)[:64].contiguous(), io="bf16")
+        n = agm.clip_grads([g["dlog_decay"], g["dh0"]], 0.5)
+        return [y, hT, g["dq"], g["dk"], g["dv"], g["dlog_decay"], g["dh0"], x, ri, n]
+
+    want = [work(t) for t in ins]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in ins]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(side):
+            with torch.cuda.stream(s):
+                got[i].append(work(ins[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            for a, b in zip(run, want[i]):
+                assert torch.equal(a, b)
+
+
+def test_an_explicit_stream_owns_what_the_call_makes(agm):
+    s = torch.cuda.Stream()
+    t = device_inputs(ref.inputs(62, 700, 1, 1, 64, 64, "bf16"), "bf16")
+    want = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"])
+    r, dx = t["g"].expand(700, 64).contiguous(), t["dy"].view(700, 64)
+    gm = torch.ones(64, device="cuda")
+    wn = agm.add_norm(r, dx, gm)
+    wg = agm.add_norm_grad(wn[1], wn[2], gm, dx)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        g = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], stream=s.cuda_stream)
+        n = agm.add_norm(r, dx, gm, stream=s.cuda_stream)
+        s.synchronize()
+        gg = agm.add_norm_grad(n[1], n[2], gm, dx, stream=s.cuda_stream)
+        norm = agm.clip_grads([gg[0]], float("inf"), stream=s.cuda_stream)
+        s.synchronize()
+        assert all(torch.equal(g[m], want[m]) for m in want)
+        assert all(torch.equal(a, b) for a, b in zip(n, wn)) and all(torch.equal(a, b) for a, b in zip(gg, wg))
+        assert abs(float(norm) - float(wg[0].double().norm())) <= 1e-6 * float(norm)
+
+
+def test_refusals_of_gpu_tensors(agm):
+    q = torch.zeros(6, 2, 16, device="cuda", dtype=torch.bfloat16)
+    v = torch.zeros(6, 4, 8, device="cuda", dtype=torch.bfloat16)
+    g = torch.zeros(6, 4, device="cuda")
+    ok = lambda **kw: agm.linattn_forward(**{**dict(q=q, k=q, v=v, log_decay=g), **kw})
+    ok()
+    off = lambda *x, dtype=torch.int32: torch.tensor(x, dtype=dtype, device="cuda")
+    for kw, word in ((dict(k=q[:5]), "shape"), (dict(k=q.float()), "dtype"), (dict(v=v[:, :, ::2]), "contiguous"),
+                     (dict(log_decay=g.double()), "dtype"), (dict(log_decay=g[:, :3]), "shape"),
+                     (dict(log_decay=torch.zeros(3, device="cuda")), "shape"),
+                     (dict(h0=torch.zeros(1, 4, 16, 9, device="cuda")), "shape"),
+                     (dict(seq_start=off(0, 6, dtype=torch.int64)), "dtype"), (dict(seq_start=off(0)), "offsets"),
+                     (dict(y=torch.zeros(6, 4, 8, device="cuda")), "dtype"), (dict(k=q.cpu()), "GPU tensor"),
+                     (dict(ws=torch.zeros(4, device="cuda")), "dtype"), (dict(q=q.half(), k=q.half()), "dtype")):
+        with pytest.raises(agm.SsmError, match=word):
+            ok(**kw)
+    with pytest.raises(agm.SsmError, match="UNSUPPORTED"):
+        agm.linattn_forward(q[:, :, :12].contiguous(), q[:, :, :12].contiguous(), v, g)
+    with pytest.raises(agm.SsmError, match="ERR_ARG"):  # two value heads for three key heads
+        agm.linattn_forward(torch.zeros(6, 3, 16, device="cuda"), torch.zeros(6, 3, 16, device="cuda"),
+                            torch.zeros(6, 4, 8, device="cuda"), g)
+    with pytest.raises(agm.SsmError, match="none of"):
+        agm.linattn_grad(q, q, v, g, v, want=["dx"])
+    with pytest.raises(agm.SsmError):
+        agm.linattn_grad(q, q, v, g, v, want=[])
+    with pytest.raises(agm.SsmError, match="shape"):
+        agm.linattn_step(q, q, v, g, torch.zeros(5, 4, 16, 8, device="cuda"))
+    with pytest.raises(agm.SsmError, match="dimensions"):
+        agm.linattn_step(q[None], q[None], v[None], g[None], torch.zeros(6, 4, 16, 8, device="cuda"))
+    r = torch.zeros(4, 8, device="cuda")
+    for call, word in ((lambda: agm.add_norm(r, r.bfloat16()[:3], torch.ones(8, device="cuda")), "shape"),
+                       (lambda: agm.add_norm(r, r.half(), torch.ones(8, device="cuda")), "io dtype"),
+                       (lambda: agm.add_norm(r, None, torch.ones(7, device="cuda"), io="f32"), "shape"),
+                       (lambda: agm.add_norm(r, None, torch.ones(8, device="cuda")), "io dtype"),
+                       (lambda: agm.add_norm(r.t(), None, torch.ones(4, device="cuda"), io="f32"), "contiguous"),
+                       (lambda: agm.add_norm_grad(r, torch.ones(3, device="cuda"), torch.ones(8, device="cuda"), r), "shape"),
+                       (lambda: agm.clip_grads([r, r], 1.0), "twice"),
+                       (lambda: agm.clip_grads([r, r.bfloat16()], 1.0), "dtype"),
+                       (lambda: agm.clip_grads([r], 0.0), "positive"),
+                       (lambda: agm.clip_grads([r], 1.0, out=[r[:2]]), "shape"),
+                       (lambda: agm.clip_grads([r], 1.0, out=[]), "outputs"),
+                       (lambda: agm.clip_grads([r.t()], 1.0), "contiguous")):
+        with pytest.raises(agm.SsmError, match=word):
+            call()
