@@ -20,44 +20,65 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kVec = 4;  // elements an access
 constexpr int64_t kMaxP = 16384;
 constexpr int64_t kMaxRows = int64_t(1) << 31;
 
 typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
 
-// VEC consecutive elements as floats.
-template <int VEC>
-__device__ __forceinline__ void load_vec(const float* p, float* o) {
-  if constexpr (VEC == 4) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(p);
-    o[0] = v[0]; o[1] = v[1]; o[2] = v[2]; o[3] = v[3];
+typedef __attribute__((__vector_size__(4 * sizeof(float)), aligned(4))) float f32x4_any;
+typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)), aligned(2))) uint32_t u32x2_any;
+typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
+
+// The next four of a row's `left` > 0 elements as floats, zeros past its end.
+// AL: rows start aligned and hold a multiple of four; otherwise the accesses
+// are aligned to the element only, and a row's last ones are single.
+template <bool AL>
+__device__ __forceinline__ void load_vec(const float* p, int left, float* o) {
+  if (AL || left >= 4) {
+    const f32x4 v = AL ? *reinterpret_cast<const f32x4*>(p) : f32x4(*reinterpret_cast<const f32x4_any*>(p));
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = v[e];
   } else {
-    o[0] = *p;
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = e < left ? p[e] : 0.0f;
   }
 }
-template <int VEC>
-__device__ __forceinline__ void load_vec(const bf16_t* p, float* o) {
-  if constexpr (VEC == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    o[0] = __uint_as_float(u.x << 16); o[1] = __uint_as_float(u.x & 0xffff0000u);
-    o[2] = __uint_as_float(u.y << 16); o[3] = __uint_as_float(u.y & 0xffff0000u);
+template <bool AL>
+__device__ __forceinline__ void load_vec(const bf16_t* p, int left, float* o) {
+  if (AL || left >= 4) {
+    const u32x2 u = AL ? *reinterpret_cast<const u32x2*>(p) : u32x2(*reinterpret_cast<const u32x2_any*>(p));
+    o[0] = __uint_as_float(u[0] << 16); o[1] = __uint_as_float(u[0] & 0xffff0000u);
+    o[2] = __uint_as_float(u[1] << 16); o[3] = __uint_as_float(u[1] & 0xffff0000u);
   } else {
-    o[0] = bf16_to_f32(*p);
+#pragma unroll
+    for (int e = 0; e < 4; e++) o[e] = e < left ? bf16_to_f32(p[e]) : 0.0f;
   }
 }
-template <int VEC>
-__device__ __forceinline__ void store_vec(float* p, const float* v) {
-  if constexpr (VEC == 4) *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-  else *p = v[0];
-}
-template <int VEC>
-__device__ __forceinline__ void store_vec(bf16_t* p, const float* v) {
-  if constexpr (VEC == 4) {
-    const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
-    const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
-    *reinterpret_cast<uint2*>(p) = uint2{a, b};
+template <bool AL>
+__device__ __forceinline__ void store_vec(float* p, int left, const float* v) {
+  if (AL) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+  } else if (left >= 4) {
+    *reinterpret_cast<f32x4_any*>(p) = f32x4_any{v[0], v[1], v[2], v[3]};
   } else {
-    *p = f32_to_bf16(v[0]);
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (e < left) p[e] = v[e];
+  }
+}
+template <bool AL>
+__device__ __forceinline__ void store_vec(bf16_t* p, int left, const float* v) {
+  const uint32_t a = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+  const uint32_t b = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+  if (AL) {
+    *reinterpret_cast<u32x2*>(p) = u32x2{a, b};
+  } else if (left >= 4) {
+    *reinterpret_cast<u32x2_any*>(p) = u32x2_any{a, b};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+      if (e < left) p[e] = static_cast<bf16_t>((e < 2 ? a : b) >> (e % 2 * 16));
   }
 }
 
@@ -77,20 +98,20 @@ __device__ __forceinline__ float row_sum(float v, float* buf) {
   return v;
 }
 
-template <class T, int TPR, int NE, int VEC>
+template <class T, int TPR, int NE, bool AL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm(
     int64_t rows, int P, const float* r, const T* __restrict__ y, const float* __restrict__ scale, float eps,
     float* r_out, T* __restrict__ x, float* __restrict__ rinv) {
   constexpr int NT = TPR > kThreads ? TPR : kThreads;
   constexpr int RW = NT / TPR;  // rows a workgroup holds at once
-  constexpr int NV = NE / VEC;
+  constexpr int NV = NE / kVec;
   __shared__ float buf[2][NT / 64];
   const int l = threadIdx.x % TPR;
   float gm[NE];
 #pragma unroll
   for (int i = 0; i < NV; i++) {
-    const int p = (l + TPR * i) * VEC;
-    if (p < P) load_vec<VEC>(scale + p, gm + i * VEC);
+    const int p = (l + TPR * i) * kVec;
+    if (p < P) load_vec<AL>(scale + p, P - p, gm + i * kVec);
   }
   const float inv_p = 1.0f / static_cast<float>(P);
   int flip = 0;
@@ -101,27 +122,27 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm(
     float v[NE], u[NE];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int p = (l + TPR * i) * VEC;
-      if (p < P) load_vec<VEC>(r + o + p, v + i * VEC);
+      const int p = (l + TPR * i) * kVec;
+      if (p < P) load_vec<AL>(r + o + p, P - p, v + i * kVec);
     }
     if (y) {
 #pragma unroll
       for (int i = 0; i < NV; i++) {
-        const int p = (l + TPR * i) * VEC;
-        if (p < P) load_vec<VEC>(y + o + p, u + i * VEC);
+        const int p = (l + TPR * i) * kVec;
+        if (p < P) load_vec<AL>(y + o + p, P - p, u + i * kVec);
       }
     }
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int p = (l + TPR * i) * VEC;
+      const int p = (l + TPR * i) * kVec;
       if (p < P) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) {
-          if (y) v[i * VEC + e] += u[i * VEC + e];
-          ss = fmaf(v[i * VEC + e], v[i * VEC + e], ss);
+        for (int e = 0; e < kVec; e++) {
+          if (y) v[i * kVec + e] += u[i * kVec + e];
+          ss = fmaf(v[i * kVec + e], v[i * kVec + e], ss);
         }
-        if (r_out) store_vec<VEC>(r_out + o + p, v + i * VEC);
+        if (r_out) store_vec<AL>(r_out + o + p, P - p, v + i * kVec);
       }
     }
     ss = row_sum<TPR>(ss, buf[flip]);
@@ -129,31 +150,31 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm(
     if (rinv && l == 0) rinv[t] = ri;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int p = (l + TPR * i) * VEC;
+      const int p = (l + TPR * i) * kVec;
       if (p < P) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) v[i * VEC + e] = gm[i * VEC + e] * (v[i * VEC + e] * ri);
-        store_vec<VEC>(x + o + p, v + i * VEC);
+        for (int e = 0; e < kVec; e++) v[i * kVec + e] = gm[i * kVec + e] * (v[i * kVec + e] * ri);
+        store_vec<AL>(x + o + p, P - p, v + i * kVec);
       }
     }
   }
 }
 
-template <class T, int TPR, int NE, int VEC>
+template <class T, int TPR, int NE, bool AL>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm_grad(
     int64_t rows, int P, const float* __restrict__ r, const float* __restrict__ rinv, const float* __restrict__ scale,
     const T* __restrict__ dx, const float* dr_out, float* dr, float* __restrict__ part) {
   constexpr int NT = TPR > kThreads ? TPR : kThreads;
   constexpr int RW = NT / TPR;
-  constexpr int NV = NE / VEC;
+  constexpr int NV = NE / kVec;
   __shared__ float buf[2][NT / 64];
   __shared__ float cols[RW > 1 ? TPR * NE : 1];
   const int l = threadIdx.x % TPR;
   float gm[NE], dg[NE];
 #pragma unroll
   for (int i = 0; i < NV; i++) {
-    const int p = (l + TPR * i) * VEC;
-    if (p < P) load_vec<VEC>(scale + p, gm + i * VEC);
+    const int p = (l + TPR * i) * kVec;
+    if (p < P) load_vec<AL>(scale + p, P - p, gm + i * kVec);
   }
 #pragma unroll
   for (int e = 0; e < NE; e++) dg[e] = 0.0f;
@@ -166,20 +187,20 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm_gr
     const float ri = rinv[t];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int p = (l + TPR * i) * VEC;
+      const int p = (l + TPR * i) * kVec;
       if (p < P) {
-        load_vec<VEC>(r + o + p, xh + i * VEC);
-        load_vec<VEC>(dx + o + p, d + i * VEC);
-        if (dr_out) load_vec<VEC>(dr_out + o + p, c + i * VEC);
+        load_vec<AL>(r + o + p, P - p, xh + i * kVec);
+        load_vec<AL>(dx + o + p, P - p, d + i * kVec);
+        if (dr_out) load_vec<AL>(dr_out + o + p, P - p, c + i * kVec);
       }
     }
     float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      if ((l + TPR * i) * VEC < P) {
+      if ((l + TPR * i) * kVec < P) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) {
-          const int k = i * VEC + e;
+        for (int e = 0; e < kVec; e++) {
+          const int k = i * kVec + e;
           xh[k] *= ri;
           dg[k] = fmaf(d[k], xh[k], dg[k]);
           d[k] *= gm[k];
@@ -190,15 +211,15 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm_gr
     m = row_sum<TPR>(m, buf[flip]) * inv_p;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-      const int p = (l + TPR * i) * VEC;
+      const int p = (l + TPR * i) * kVec;
       if (p < P) {
 #pragma unroll
-        for (int e = 0; e < VEC; e++) {
-          const int k = i * VEC + e;
+        for (int e = 0; e < kVec; e++) {
+          const int k = i * kVec + e;
           const float g = ri * fmaf(-xh[k], m, d[k]);
           d[k] = dr_out ? c[k] + g : g;
         }
-        store_vec<VEC>(dr + o + p, d + i * VEC);
+        store_vec<AL>(dr + o + p, P - p, d + i * kVec);
       }
     }
   }
@@ -225,9 +246,9 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void k_add_norm_gr
 #pragma unroll
     for (int i = 0; i < NV; i++)
 #pragma unroll
-      for (int e = 0; e < VEC; e++) {
-        const int p = (l + TPR * i) * VEC + e;
-        if (p < P) q[p] = dg[i * VEC + e];
+      for (int e = 0; e < kVec; e++) {
+        const int p = (l + TPR * i) * kVec + e;
+        if (p < P) q[p] = dg[i * kVec + e];
       }
   }
 }
@@ -251,18 +272,22 @@ __global__ __launch_bounds__(256) void k_column_sums(int nb, int P, const float*
   }
 }
 
-// Lanes a row and elements a lane.  Four rows a workgroup (64 lanes each)
-// when there are rows to fill the chip, else one row over 256 lanes, for the
-// shorter chain of loads; wide rows need the lanes for their registers.
+// Lanes a row and elements a lane: eight elements (sixteen for the widest
+// rows) and as many lanes as the row needs, in steps; more elements a lane
+// leave fewer wavefronts in flight (65536 rows of 2048: 298 us with 256 lanes
+// of 8, 352 with 64 of 32).  Narrow rows go four to a workgroup if there are
+// many (65536 rows of 512: 77 us with 64 lanes a row, 83 with 256; 64 rows:
+// 3.2 and 2.9).
 struct Shape {
   int tpr, ne, rows_wg;
 };
 
 Shape shape_for(int64_t T, int64_t P) {
-  if (P <= 2048 && T >= 2048) return P <= 512 ? Shape{64, 8, 4} : Shape{64, 32, 4};
+  if (P <= 512 && T >= 1024) return Shape{64, 8, 4};
   if (P <= 2048) return Shape{256, 8, 1};
-  if (P <= 8192) return Shape{256, 32, 1};
-  return Shape{512, 32, 1};
+  if (P <= 4096) return Shape{512, 8, 1};
+  if (P <= 8192) return Shape{1024, 8, 1};
+  return Shape{1024, 16, 1};
 }
 
 constexpr int64_t kFwdWgs = 4096, kGradWgs = 1024;
@@ -286,36 +311,36 @@ struct NormArgs {
   float* part;
 };
 
-template <bool GRAD, class T, int TPR, int NE, int VEC>
+template <bool GRAD, class T, int TPR, int NE, bool AL>
 hipError_t launch_shape(const NormArgs& a, unsigned grid, hipStream_t st) {
   constexpr int NT = TPR > kThreads ? TPR : kThreads;
   if constexpr (GRAD)
-    k_add_norm_grad<T, TPR, NE, VEC><<<grid, NT, 0, st>>>(a.T, static_cast<int>(a.P), a.r, a.rinv_in, a.scale,
+    k_add_norm_grad<T, TPR, NE, AL><<<grid, NT, 0, st>>>(a.T, static_cast<int>(a.P), a.r, a.rinv_in, a.scale,
                                                         static_cast<const T*>(a.y), a.dr_out, a.r_out, a.part);
   else
-    k_add_norm<T, TPR, NE, VEC><<<grid, NT, 0, st>>>(a.T, static_cast<int>(a.P), a.r, static_cast<const T*>(a.y),
+    k_add_norm<T, TPR, NE, AL><<<grid, NT, 0, st>>>(a.T, static_cast<int>(a.P), a.r, static_cast<const T*>(a.y),
                                                    a.scale, a.eps, a.r_out, static_cast<T*>(a.x), a.rinv);
   return hipGetLastError();
 }
 
-template <bool GRAD, class T, int VEC>
+template <bool GRAD, class T, bool AL>
 hipError_t launch_vec(const NormArgs& a, const Shape& s, unsigned grid, hipStream_t st) {
-  if (s.tpr == 64) return s.ne == 8 ? launch_shape<GRAD, T, 64, 8, VEC>(a, grid, st)
-                                    : launch_shape<GRAD, T, 64, 32, VEC>(a, grid, st);
-  if (s.tpr == 256) return s.ne == 8 ? launch_shape<GRAD, T, 256, 8, VEC>(a, grid, st)
-                                     : launch_shape<GRAD, T, 256, 32, VEC>(a, grid, st);
-  return launch_shape<GRAD, T, 512, 32, VEC>(a, grid, st);
+  if (s.tpr == 64) return launch_shape<GRAD, T, 64, 8, AL>(a, grid, st);
+  if (s.tpr == 256) return launch_shape<GRAD, T, 256, 8, AL>(a, grid, st);
+  if (s.tpr == 512) return launch_shape<GRAD, T, 512, 8, AL>(a, grid, st);
+  if (s.ne == 8) return launch_shape<GRAD, T, 1024, 8, AL>(a, grid, st);
+  return launch_shape<GRAD, T, 1024, 16, AL>(a, grid, st);
 }
 
 // Rows of P elements start 16 bytes aligned in float32, 8 in bfloat16, when P
-// is a multiple of 4: four elements an access then, else one.
+// is a multiple of 4.  (65536 rows of 999: 181 us; 305 with one element an access.)
 template <bool GRAD>
 hipError_t launch_norm(const NormArgs& a, bool bf16, hipStream_t st) {
   const Shape s = shape_for(a.T, a.P);
   const unsigned grid = grid_for(s, a.T, GRAD ? kGradWgs : kFwdWgs);
   if (a.P % 4 == 0)
-    return bf16 ? launch_vec<GRAD, bf16_t, 4>(a, s, grid, st) : launch_vec<GRAD, float, 4>(a, s, grid, st);
-  return bf16 ? launch_vec<GRAD, bf16_t, 1>(a, s, grid, st) : launch_vec<GRAD, float, 1>(a, s, grid, st);
+    return bf16 ? launch_vec<GRAD, bf16_t, true>(a, s, grid, st) : launch_vec<GRAD, float, true>(a, s, grid, st);
+  return bf16 ? launch_vec<GRAD, bf16_t, false>(a, s, grid, st) : launch_vec<GRAD, float, false>(a, s, grid, st);
 }
 
 ssm_status check_sizes(int64_t T, int64_t P) {

@@ -9,8 +9,8 @@
 // last, and the caches still hold, is read first.
 //
 // Few elements (kSmall, in a few tensors) are one workgroup's work: it adds
-// and then scales in one launch, which costs less than the second launch
-// would.
+// and then scales in one launch (fp32, 4 tensors: 16000 elements 5.1 us against
+// 8.4 us for two launches, 64000 9.7 against 11.6, 128000 14.7 against 11.1).
 //
 // The tensor table travels in the kernel arguments, kTable tensors a launch:
 // nothing is copied to the device, and a captured launch keeps its own.
@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kTable = 96;             // tensors a launch (3 KB of arguments)
 constexpr int kBlock = 8192;           // elements a workgroup takes at a time
-constexpr int64_t kSmall = 32768;      // elements of the one-launch form,
+constexpr int64_t kSmall = 65536;      // elements of the one-launch form,
 constexpr int kSmallCount = 16;        // which walks its tensors one by one
 constexpr int64_t kMaxWgs = 1024;      // per launch: also its partial sums
 constexpr int32_t kMaxTensors = 65536;

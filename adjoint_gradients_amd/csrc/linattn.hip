@@ -358,23 +358,29 @@ ssm_status check_in(const ssm_linattn_dims* d, const ssm_linattn_in* in) {
   return SSM_OK;
 }
 
-// Tokens per segment.  A run walks its segment chunk by chunk.  Segments are
-// short enough for kRounds workgroups for each that fits on the chip at once
-// (some take a third longer than others, and the last round hides it), but of
-// at least kMinChunks chunks: a segment costs one more read of two of its
-// operands and two passes over a state.  Without room for two segments there
-// is one per sequence, and neither of those passes.
+// Tokens per segment.  A run walks its segment chunk by chunk, and a segment
+// costs one more read of two of its operands and two passes over a state.
+// With much work a segment is a quarter of what a workgroup would have if all
+// of them ran at once (kRounds: some XCDs are a sixth slower, and the later
+// rounds even that out), of at least kChunks chunks; with little, it is as
+// short as still gives every place on the chip one, down to kMinChunks.
+// Gradient of 65536 tokens, 16 heads of 128: 1.78, 1.62, 1.52, 1.53 ms with 1,
+// 2, 4, 8 rounds.  8192 tokens: 271, 245, 214, 258 us with segments of 2, 4,
+// 8, 16 chunks; forward of 2048 tokens: 36, 40, 60, 105 us.
 constexpr int64_t kCus = 256;
 constexpr int64_t kRounds = 4;
-constexpr int64_t kMinChunks = 4;
+constexpr int64_t kChunks = 8, kMinChunks = 2;
 
 int64_t longest(const ssm_linattn_dims* d, bool packed) { return packed ? d->T : d->T / d->S; }
 
 int64_t segment_tokens(const ssm_linattn_dims* d, bool packed, int runs) {
   const int64_t ch = chunk_tokens(d->io == SSM_BF16);
-  const int64_t wgs = kRounds * kCus * (padded(d->dk) * padded(d->dv) > 64 * 64 ? 2 : 3);
-  int64_t L = (d->T * d->Hv * runs / wgs + ch - 1) / ch * ch;
-  if (L < kMinChunks * ch) L = kMinChunks * ch;
+  const int64_t places = kCus * (padded(d->dk) * padded(d->dv) > 64 * 64 ? 2 : 3);
+  const int64_t work = d->T * d->Hv * runs / ch;  // chunks of all heads and runs
+  const int64_t one_round = (work + places - 1) / places;
+  int64_t chunks = one_round < kMinChunks ? kMinChunks : one_round < kChunks ? one_round : kChunks;
+  if (chunks < work / (places * kRounds)) chunks = work / (places * kRounds);
+  const int64_t L = chunks * ch;
   const int64_t n = (longest(d, packed) + ch - 1) / ch * ch;
   return L < n ? L : n;
 }
@@ -451,14 +457,10 @@ bool any_grad(const ssm_linattn_grads* g) { return g->dq || g->dk || g->dv || g-
 
 // Launches the runs of a kernel that have operands.
 hipError_t launch(Kernel k, const ssm_linattn_dims* d, Args& a, hipStream_t st) {
-  // Heads that share q and k stay on one XCD where that still leaves each of
-  // the 8 XCDs several units of work.
-  const int64_t slots = slot_count(d->T, d->S, a.sq.L);
   a.nz = 0;
   for (int i = 0; i < 3; i++)
     if (a.run[i].K) a.run_of[a.nz++] = i;
-  a.unit_heads = slots * d->Hk >= 64 ? d->Hv / d->Hk : 1;
-  a.units = static_cast<uint32_t>(slots * (d->Hv / a.unit_heads));
+  a.units = static_cast<uint32_t>(slot_count(d->T, d->S, a.sq.L) * d->Hv);
   const bool wide = padded(d->dk) == 128;
   if (d->io == SSM_BF16) return wide ? launch_bf16_128(k, d->dv, a, st) : launch_bf16_64(k, d->dv, a, st);
   return wide ? launch_f32_128(k, d->dv, a, st) : launch_f32_64(k, d->dv, a, st);

@@ -49,8 +49,7 @@ struct Args {
   int32_t sum_heads;               // dq and dk are float32, one per value head
   int32_t nz;                      // runs of the launch,
   int32_t run_of[3];               // and which they are
-  int32_t unit_heads;              // consecutive heads whose workgroups stay on one XCD
-  uint32_t units;                  // segment slots x Hv / unit_heads
+  uint32_t units;                  // segment slots x heads
   Run run[3];
 };
 

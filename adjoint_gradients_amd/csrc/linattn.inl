@@ -838,24 +838,22 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 }
 
 // The workgroup's segment, head and run.  Workgroups go round-robin over the
-// 8 XCDs; the runs of one head, which read the same rows, and with enough of
-// them the heads that share q and k, follow one another on one XCD and find
-// the rows in its L2.
+// 8 XCDs: the runs of one head, which read the same rows, follow one another
+// on one XCD and find the rows in its L2.
 struct Work {
   uint32_t slot;
   int h, z;
   bool any;
 };
 
-__device__ __forceinline__ Work work_of(const Args& a, int nz) {
-  const uint32_t unit_wgs = static_cast<uint32_t>(a.unit_heads * nz);
-  const uint32_t i = blockIdx.x / 8, u = i / unit_wgs * 8 + blockIdx.x % 8, k = i % unit_wgs;
-  const uint32_t per_slot = static_cast<uint32_t>(a.Hv / a.unit_heads);
+__device__ __forceinline__ Work work_of(const Args& a) {
+  const uint32_t nz = static_cast<uint32_t>(a.nz);
+  const uint32_t i = blockIdx.x / 8, u = i / nz * 8 + blockIdx.x % 8;
   Work w;
   w.any = u < a.units;
-  w.slot = u / per_slot;
-  w.h = static_cast<int>(u % per_slot * a.unit_heads + k / nz);
-  w.z = a.run_of[k % nz];
+  w.slot = u / static_cast<uint32_t>(a.Hv);
+  w.h = static_cast<int>(u % static_cast<uint32_t>(a.Hv));
+  w.z = a.run_of[i % nz];
   return w;
 }
 
@@ -871,7 +869,7 @@ constexpr int wgs_per_cu(int dk, int dv, int kind) {
 template <class T, class PT, int DK, int DV, int KIND>
 __global__ __launch_bounds__(kThreads, wgs_per_cu(DK, DV, KIND)) void k_linattn(Args a) {
   extern __shared__ __attribute__((aligned(16))) char smem_la[];
-  const Work w = work_of(a, a.nz);
+  const Work w = work_of(a);
   if (!w.any) return;
   constexpr int P2 = 2;
   if constexpr (KIND == kForward) {
@@ -909,7 +907,7 @@ hipError_t launch_one(const Args& a, hipStream_t st) {
         hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  const uint32_t grid = (a.units + 7) / 8 * 8 * static_cast<uint32_t>(a.unit_heads * a.nz);
+  const uint32_t grid = (a.units + 7) / 8 * 8 * static_cast<uint32_t>(a.nz);
   kern<<<grid, kThreads, lds, st>>>(a);
   return hipGetLastError();
 }
