@@ -8,7 +8,8 @@ rows of q, k [T, Hk, dk] and v [T, Hv, dv] (Hk divides Hv; value head h reads
 key head h // (Hv // Hk)); rows may be strided, heads and channels not.
 Sequences are packed (seq_start, offsets on the GPU), or equally long when the
 tensors are [S, L, H, d].  log_decay is float32, [T, Hv] or, one for each head,
-[Hv]; states are float32 [S, Hv, dk, dv].
+[Hv]; states are float32 [S, Hv, dk, dv].  Output tensors that a caller gives
+overlap no input and no other output, except hT, which may be h0.
 
 Every tensor of a call lives on one GPU; work goes to that GPU's current
 stream, or to the raw handle `stream`, on which tensors that the call makes

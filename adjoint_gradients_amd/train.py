@@ -1,4 +1,8 @@
-"""The residual update with its norm, and gradient clipping (include/ssm_train.h)."""
+"""The residual update with its norm, and gradient clipping (include/ssm_train.h).
+
+Output tensors that a caller gives overlap no input and no other output,
+except where a function says so.
+"""
 from __future__ import annotations
 
 import ctypes
@@ -125,8 +129,8 @@ def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
     before that, a float32 tensor [1] on the GPU (nothing is synchronised).
     grads: tensors, or dicts of tensors as adjoint_grad, stack_grad and
     linattn_grad return them, all of one dtype (float32 or bfloat16) on one
-    GPU.  They are scaled in place, or into the tensors `out`; a norm that is
-    not finite leaves them as they are.  max_norm = inf only measures."""
+    GPU.  They are scaled in place, or into the tensors `out`, each of which may
+    be its own gradient; a norm that is not finite leaves them as they are.  max_norm = inf only measures."""
     ts = []
     for g in grads:
         if isinstance(g, dict):
@@ -157,7 +161,12 @@ def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
         if len(out) != n:
             _bad(f"clip_grads: {len(out)} outputs for {n} gradients")
         po = _addresses(out, "an output", device, dt)
-        for o, t in zip(out, ts):
+        source = {p: i for i, (p, t) in enumerate(zip(pi, ts)) if t.numel()}
+        if len({p for p, t in zip(po, ts) if t.numel()}) != sum(1 for t in ts if t.numel()):
+            _bad("clip_grads: an output is given twice")
+        for i, (o, t) in enumerate(zip(out, ts)):
+            if t.numel() and source.get(po[i], i) != i:
+                _bad("clip_grads: an output is another gradient")
             if o.shape != t.shape:
                 _bad(f"an output: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
     ptrs, counts = _VP * n, _I64 * n

@@ -87,7 +87,8 @@ ssm_status ssm_linattn_grad(const ssm_linattn_dims *dims, const ssm_linattn_in *
 
 /* One token for each of dims.T sequences (S is not read): row t is the next
  * token of the sequence whose state is state[t] ([T][Hv][dk][dv]), which is
- * updated in place.  in->seq_start and in->h0 must be NULL.  No workspace. */
+ * updated in place.  in->seq_start and in->h0 must be NULL; y must not overlap
+ * an input.  No workspace. */
 ssm_status ssm_linattn_step(const ssm_linattn_dims *dims, const ssm_linattn_in *in, float *state, void *y, int64_t ldy,
                             void *stream);
 

@@ -5,7 +5,8 @@
  * the conventions of ssm_adjoint.h hold (device pointers owned by the caller,
  * 16-byte aligned; nothing allocated or synchronised; complete validation
  * before anything is enqueued; outputs overwritten; bitwise repeatable
- * results; SSM_* status codes).
+ * results; SSM_* status codes).  An output overlaps no input and no other
+ * output except where it says so below.
  */
 #ifndef SSM_TRAIN_H
 #define SSM_TRAIN_H

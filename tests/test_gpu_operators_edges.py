@@ -180,3 +180,19 @@ def test_refusals_of_gpu_tensors(agm):
                        (lambda: agm.clip_grads([r.t()], 1.0), "contiguous")):
         with pytest.raises(agm.SsmError, match=word):
             call()
+
+
+def test_clip_outputs_that_meet(agm):
+    """One output for two gradients, and an output that is another gradient: refused, nothing written."""
+    a, b, c = (torch.full((40,), float(i + 1), device="cuda") for i in range(3))
+    none = torch.empty(0, device="cuda")
+    for ts, out in (([a, b], [c, c]), ([a, b], [b, c]), ([a, a], [a, c])):
+        with pytest.raises(agm.SsmError):
+            agm.clip_grads(ts, 1.0, out=out)
+    assert [float(t.sum()) for t in (a, b, c)] == [40.0, 80.0, 120.0]
+    # in place beside a separate output, the same input twice, empty tensors at one address
+    n = agm.clip_grads([a, b, none, none], 1.0, out=[a, c, none, none])
+    assert abs(float(n) - (40 * 1 + 40 * 4) ** 0.5) < 1e-4
+    d, e = torch.empty_like(b), torch.empty_like(b)
+    agm.clip_grads([b, b], 1e9, out=[d, e])
+    assert torch.equal(d, b) and torch.equal(e, b)
