@@ -642,7 +642,10 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 
       if constexpr (kDg) keep_state(c);
       // the next chunk's loads: after the scores, whose registers they take
-      // (with the decay gradient's operands, after the output, which takes more)
+      // (with the decay gradient's operands, after the state's part, which
+      // takes more, and in fp32 after the product with V: 65536 bf16 tokens,
+      // 16 heads of 128 take 1.47 ms, 1.50 after that product; 32768 fp32
+      // tokens 1.72 ms, 1.70 after it)
       if constexpr (!kDg) issue(REV ? c - 1 : c + 1, it + 1 < nch);
 
       // the state's part, transposed: rows n of this wavefront, columns i
@@ -712,7 +715,12 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     }
     if constexpr (MODE != kAgg) lds_barrier();  // scores and partial sums are in LDS
 
-    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kDg && kBf) {
+      issue(REV ? c - 1 : c + 1, it + 1 < nch);
+      issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
+    } else {
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // V of this wavefront's columns, tokens along the lane's elements
     if constexpr (kBf) {
       bf16x8_t vf[CH / 32][NB];
@@ -732,11 +740,6 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 #pragma unroll
               for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
             }
-        if constexpr (kDg) {
-          __builtin_amdgcn_sched_barrier(0);
-          issue(REV ? c - 1 : c + 1, it + 1 < nch);
-          issue_x(REV ? c - 1 : c + 1, it + 1 < nch);
-        }
         put(tb, nv, Y);
       }
       __builtin_amdgcn_sched_barrier(0);
