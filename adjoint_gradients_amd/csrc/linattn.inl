@@ -32,13 +32,14 @@
 // go through LDS; the next chunk's tiles are loaded into registers while the
 // current one is computed.
 //
-// Rounding: products are bf16 x bf16 summed in fp32 (or fp32 throughout).
-// The decayed scores are rounded to bf16 before they multiply V, and the
-// state to bf16 where it multiplies Q: both errors are of the size of the
-// output's own rounding.  Where a product ends in an fp32 output (states,
-// decay gradient), its fp32 operand is split into bf16 parts that together
-// hold it whole: the weighted V of the state's update, and the state in the
-// runs that form the decay gradient.
+// Rounding: products are bf16 x bf16 summed in fp32 (or fp32 throughout).  An
+// fp32 operand of one (the decayed scores, the state, the weighted V) is
+// split into bf16 parts: two where the product only reaches bf16 outputs, so
+// that their own rounding is all they are off by; three, which hold it whole,
+// where it ends in an fp32 output (states, decay gradient).  With one part a
+// few tokens, whose sums do not average the roundings, were off by up to 3.5e-3
+// where the output's rounding is 1.5e-3; the second part costs the forward
+// pass of 65536 tokens, 16 heads of 128, 2% (475 -> 484 us), its gradient 2%.
 #include "linattn_seqs.hpp"
 #include "ssm_common.hpp"
 
@@ -61,9 +62,9 @@ constexpr int kAgg = 1;       // only the state's sum over the segment
 constexpr int kOutFwdDg = 2;  // out, the decay gradient's terms of the pairs that end here, the anchor states
 constexpr int kOutRevDg = 3;  // out, the terms of the pairs that start here, the anchor states' adjoints
 
-// bf16 parts of an fp32 operand whose product ends in an fp32 output: three
-// hold all 24 bits.
-constexpr int kParts = 3;
+// bf16 parts of an fp32 operand of a product: three hold all 24 bits, for an
+// fp32 output; two, off by 2^-17, for a bf16 one.
+constexpr int kParts = 3, kOutParts = 2;
 
 template <class T>
 struct Cfg {
@@ -84,7 +85,7 @@ struct Lds {
   static constexpr int k = q + (MODE == kAgg ? 0 : C::CH * PM * (int)sizeof(T));
   static constexpr int v = k + C::CH * PM * (int)sizeof(T);
   static constexpr int p = v + C::CH * PN * (int)sizeof(T);
-  static constexpr int f = p + (MODE == kAgg ? 0 : C::CH * C::CH * (int)sizeof(T));
+  static constexpr int f = p + (MODE == kAgg ? 0 : C::CH * C::CH * (int)sizeof(T) * (C::kBf ? kOutParts : 1));
   // two buffers of gh, gl, wq, wk and of wc; then the decay gradient's partial sums
   static constexpr int kDecay = 4 * C::CH;
   static constexpr int wc = 2 * kDecay;
@@ -107,8 +108,9 @@ __device__ __forceinline__ int at(int r, int c) {
   return r * (D + Cfg<T>::kPad) + c;
 }
 
-// Element (i, j) of the scores, without padding (two workgroups a CU need the
-// space): a row's 16-byte chunks are permuted instead.
+// Element (i, j) of the scores (bf16: of each part's CH x CH), without padding
+// (two workgroups a CU need the space): a row's 16-byte chunks are permuted
+// instead.
 template <class T>
 __device__ __forceinline__ int at_p(int i, int j) {
   constexpr int EPV = Cfg<T>::EPV;
@@ -294,6 +296,13 @@ __device__ __forceinline__ bf16x8_t take_part(float (&v)[8], bool more) {
   return __builtin_bit_cast(bf16x8_t, p);
 }
 
+__device__ __forceinline__ uint2 take_part(f32x4_t& v) {
+  const uint2 p{pack2(v[0], v[1]), pack2(v[2], v[3])};
+  v -= f32x4_t{__uint_as_float(p.x << 16), __uint_as_float(p.x & 0xffff0000u), __uint_as_float(p.y << 16),
+               __uint_as_float(p.y & 0xffff0000u)};
+  return p;
+}
+
 // Four output elements at a byte offset of a row range.
 __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t voff, f32x4_t v, float*) {
   __builtin_amdgcn_raw_buffer_store_b128(
@@ -303,9 +312,10 @@ __device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t rs, uint32_t v
   typedef __attribute__((__vector_size__(2 * sizeof(uint32_t)))) uint32_t u32x2;
   __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, rs, voff, 0, 0);
 }
+
 // OT: type of the output rows, the io type or float.  PARTS: bf16 parts of
 // the weighted V in the state's update, kParts where the state is an fp32
-// output, two (2^-17) where it only reaches bf16 outputs.
+// output, kOutParts where it only reaches bf16 outputs.
 template <class T, class OT, int DM, int DN, bool REV, int MODE, int PARTS>
 __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, int h, char* smem) {
   using C = Cfg<T>;
@@ -314,6 +324,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   constexpr int CH = C::CH, NIB = C::NIB, JW = C::JW;
   constexpr int MB = DM / 16, NB = DN / 64;
   constexpr bool kDg = MODE >= kOutFwdDg;
+  constexpr int kStateParts = kDg ? kParts : kOutParts;
   constexpr int kDecayWave = REV ? 3 : 0;  // the wavefront with the fewest score blocks
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -547,7 +558,11 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
       // the blocks that the mask leaves, and zeros in the other block of the
       // 32 columns that the product with V takes at once
       if constexpr (kBf) {
-        if ((ib & 1) == (REV ? 1 : 0)) store4(sP + at_p<T>(i, 16 * (REV ? ib - 1 : ib + 1) + 4 * g), f32x4_t{0.f, 0.f, 0.f, 0.f});
+        if ((ib & 1) == (REV ? 1 : 0)) {
+#pragma unroll
+          for (int part = 0; part < kOutParts; part++)
+            store4(sP + part * CH * CH + at_p<T>(i, 16 * (REV ? ib - 1 : ib + 1) + 4 * g), f32x4_t{0.f, 0.f, 0.f, 0.f});
+        }
       }
       // operands of a block, read one block ahead
       constexpr int KF = DM * (int)sizeof(T) / 64, VF = MODE == kOutFwdDg ? DN * (int)sizeof(T) / 64 : 1;
@@ -623,7 +638,13 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
               colsum[e] = m;
             }
           }
-          store4(sP + at_p<T>(i, 16 * jb + 4 * g), p);
+          if constexpr (kBf) {
+#pragma unroll
+            for (int part = 0; part < kOutParts; part++)
+              *reinterpret_cast<uint2*>(sP + part * CH * CH + at_p<T>(i, 16 * jb + 4 * g)) = take_part(p);
+          } else {
+            store4(sP + at_p<T>(i, 16 * jb + 4 * g), p);
+          }
           if constexpr (MODE == kOutFwdDg) {
             float s = 0.0f;
 #pragma unroll
@@ -668,8 +689,8 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 #pragma unroll
             for (int e = 0; e < 8; e++) s[e] = S[2 * kb + e / 4][nb][e % 4];
 #pragma unroll
-            for (int part = 0; part < (kDg ? kParts : 1); part++) {
-              const bf16x8_t sf = take_part(s, part + 1 < kParts);
+            for (int part = 0; part < kStateParts; part++) {
+              const bf16x8_t sf = take_part(s, part + 1 < kStateParts);
 #pragma unroll
               for (int b = 0; b < NIB; b++) Y[nb][b] = mfma_bf16(sf, qf[b], Y[nb][b]);
             }
@@ -736,9 +757,14 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
 #pragma unroll
           for (int kb = 0; kb < CH / 32; kb++)
             if (REV ? 2 * kb + 1 >= b : 2 * kb <= b) {
-              const bf16x8_t pf = load44(sP + at_p<T>(16 * b + l15, 32 * kb + 4 * g), sP + at_p<T>(16 * b + l15, 32 * kb + 16 + 4 * g));
 #pragma unroll
-              for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
+              for (int part = 0; part < kOutParts; part++) {
+                const T* const sp = sP + part * CH * CH;
+                const bf16x8_t pf = load44(sp + at_p<T>(16 * b + l15, 32 * kb + 4 * g),
+                                           sp + at_p<T>(16 * b + l15, 32 * kb + 16 + 4 * g));
+#pragma unroll
+                for (int nb = 0; nb < NB; nb++) Y[nb][b] = mfma_bf16(vf[kb][nb], pf, Y[nb][b]);
+              }
             }
         put(tb, nv, Y);
       }
@@ -874,9 +900,8 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(DK, DV, KIND)) void k_linattn(
   extern __shared__ __attribute__((aligned(16))) char smem_la[];
   const Work w = work_of(a);
   if (!w.any) return;
-  constexpr int P2 = 2;
   if constexpr (KIND == kForward) {
-    run<T, T, DK, DV, false, kOut, P2>(a, a.run[0], w.slot, w.h, smem_la);
+    run<T, T, DK, DV, false, kOut, kOutParts>(a, a.run[0], w.slot, w.h, smem_la);
   } else if constexpr (KIND == kForwardState) {
     run<T, T, DK, DV, false, kOut, kParts>(a, a.run[0], w.slot, w.h, smem_la);
   } else if constexpr (KIND == kAggregate) {
@@ -884,9 +909,9 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(DK, DV, KIND)) void k_linattn(
     else run<T, T, DK, DV, true, kAgg, kParts>(a, a.run[1], w.slot, w.h, smem_la);
   } else {
     constexpr bool dg = KIND == kGradDecay;
-    if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut, dg ? kParts : P2>(a, a.run[0], w.slot, w.h, smem_la);
+    if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut, dg ? kParts : kOutParts>(a, a.run[0], w.slot, w.h, smem_la);
     else if (w.z == 1) run<T, PT, DV, DK, true, dg ? kOutRevDg : kOut, kParts>(a, a.run[1], w.slot, w.h, smem_la);
-    else run<T, T, DK, DV, true, kOut, P2>(a, a.run[2], w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kOut, kOutParts>(a, a.run[2], w.slot, w.h, smem_la);
   }
 }
 

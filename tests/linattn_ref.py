@@ -2,14 +2,12 @@
 the tolerances of the GPU tests.
 
 Tolerances count roundings.  A value rounded to bf16 is off by at most half a
-step, 2^-8 of itself, and by 2^-8 / sqrt(3) in the mean square.  A bf16 output
-has three of them that matter: its own, the decayed scores' and the state's
-(as operands of a product), together at most 2^-8 in the mean square.  At one
-element their sum is at most 2^-8 (|y| + 2 |y|_abs), |y|_abs the same sum over
-absolute values (fp32 sums add far less).  What is fp32 but made from bf16
-inputs keeps two bf16 parts of each operand, 2^-16 of it: at most two such
-operands meet, with a mean square under 2^-16.  In fp32 a result of n sums is
-off by about sqrt(n) 2^-24, n a few thousand here: 2^-18."""
+step, 2^-8 of itself.  A bf16 output has that one rounding, whose mean square
+is at most 2^-8; its operands that are not bf16 (decayed scores, state,
+weighted v) keep two bf16 parts, 2^-17 of them, and two such operands meet at
+most.  What is fp32 but made from bf16 inputs keeps three parts of each; its
+bound, 2^-16 in the mean square, would hold with two.  In fp32 a result of n
+sums is off by about sqrt(n) 2^-24, n a few thousand here: 2^-18."""
 import numpy as np
 import torch
 

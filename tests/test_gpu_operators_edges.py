@@ -196,3 +196,31 @@ def test_clip_outputs_that_meet(agm):
     d, e = torch.empty_like(b), torch.empty_like(b)
     agm.clip_grads([b, b], 1e9, out=[d, e])
     assert torch.equal(d, b) and torch.equal(e, b)
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,dk,dv,states", [
+    ([1], 2, 4, 64, 64, False), ([1, 1], 3, 3, 8, 104, True), ([5, 2], 1, 6, 40, 24, True),
+    ([19], 2, 2, 128, 128, False), ([130, 64], 1, 2, 72, 128, True)])
+def test_bf16_rounded_once(agm, lens, Hk, Hv, dk, dv, states):
+    """Every bf16 output is off by its own rounding, half a step (2^-8 of it at
+    most), and by 2^-15 of the sum's absolute values: two operands in two bf16
+    parts each, 2^-17 apiece, and the fp32 sums (under 2^-16 for these lengths)."""
+    spans = spans_of(lens, 0)
+    T = spans[-1][1]
+    d = ref.inputs(60, T, Hk, Hv, dk, dv, "bf16", S=len(lens), states=states)
+    mag = {n: (x if n == "g" or x is None else x.abs()) for n, x in d.items()}
+    t = device_inputs(d, "bf16")
+    off = starts(spans)
+    y, _ = agm.linattn_forward(t["q"], t["k"], t["v"], t["g"], seq_start=off, h0=t["h0"], scale=0.3)
+    got = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], seq_start=off, h0=t["h0"], dhT=t["dhT"], scale=0.3)
+    plain = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], seq_start=off, h0=t["h0"], dhT=t["dhT"], scale=0.3,
+                             want=["dq", "dk", "dv"])
+    refs = []
+    for x in (d, mag):
+        r, _ = ref.gradient(x["q"], x["k"], x["v"], x["g"], x["dy"], spans, 0.3, x["h0"], x["dhT"])
+        refs.append({"y": ref.forward(x["q"], x["k"], x["v"], x["g"], spans, 0.3, x["h0"])[0], **r})
+    for n, out in (("y", [y]), ("dq", [got["dq"], plain["dq"]]), ("dk", [got["dk"], plain["dk"]]),
+                   ("dv", [got["dv"], plain["dv"]])):
+        for o in out:
+            over = (o.double().cpu() - refs[0][n]).abs() - 2.0 ** -8 * refs[0][n].abs() - 2.0 ** -15 * refs[1][n]
+            assert float(over.max()) <= 0, (n, float(over.max()))
