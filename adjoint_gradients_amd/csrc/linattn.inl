@@ -86,10 +86,13 @@ struct Lds {
   static constexpr int v = k + C::CH * PM * (int)sizeof(T);
   static constexpr int p = v + C::CH * PN * (int)sizeof(T);
   static constexpr int f = p + (MODE == kAgg ? 0 : C::CH * C::CH * (int)sizeof(T) * (C::kBf ? kOutParts : 1));
-  // two buffers of gh, gl, wq, wk and of wc; then the decay gradient's partial sums
+  // Two buffers of wc in the padding of V's last row: 16 bytes more, and three
+  // workgroups of 64-wide heads with the decay gradient would not fit a CU
+  // (LDS is given out in steps of 1280 bytes).
+  static constexpr int wc = p - C::kPad * (int)sizeof(T);
+  // two buffers of gh, gl, wq and wk; then the decay gradient's partial sums
   static constexpr int kDecay = 4 * C::CH;
-  static constexpr int wc = 2 * kDecay;
-  static constexpr int red = wc + 4;
+  static constexpr int red = 2 * kDecay;
   static constexpr int kSums = (4 + C::JW + C::NIB) * C::CH;  // two buffers of them too
   static constexpr int floats = red + (MODE >= kOutFwdDg ? 2 * kSums : 0);
   static constexpr int bytes = f + floats * 4;
@@ -340,6 +343,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
   T* const sV = reinterpret_cast<T*>(smem + M::v);
   T* const sP = reinterpret_cast<T*>(smem + M::p);
   float* const sF = reinterpret_cast<float*>(smem + M::f);
+  float* const sW = reinterpret_cast<float*>(smem + M::wc);
   const int n0 = wave * 16 * NB;  // this wavefront's state columns
 
   // the state entering the segment
@@ -435,7 +439,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
       o[2 * CH + lane] = r.qs * (REV ? er : eg);
       o[3 * CH + lane] = r.ks * (REV ? eg : er);
     }
-    if (lane == 0) sF[M::wc + buf] = exp2_split(tot);
+    if (lane == 0) sW[buf] = exp2_split(tot);
   };
 
   // Anchor states and their adjoints lie as the accumulators hold them.
@@ -532,7 +536,7 @@ __device__ __forceinline__ void run(const Args& a, const Run& r, uint32_t slot, 
     // what this chunk waits for comes before the next one's loads
     issue_decay(REV ? c - 1 : c + 1, it + 1 < nch);
     if constexpr (MODE == kAgg) issue(REV ? c - 1 : c + 1, it + 1 < nch);
-    const float wc = sF[M::wc + buf];
+    const float wc = sW[buf];
 
     f32x4_t Y[NB][NIB];
     if constexpr (MODE != kAgg) {
