@@ -6,7 +6,8 @@
 // sum nor the size of the gradients costs digits), then the scaling, each of
 // whose workgroups first adds the partial sums in the same fixed order.  The
 // scaling walks the tensors from the end, so that what the first pass read
-// last, and the caches still hold, is read first.
+// last, and the caches still hold, is read first.  51.5 million fp32 elements in
+// 60 tensors: 42 us and 68 us (0.21 GB read; 0.21 read and 0.21 written).
 //
 // Few elements (kSmall, in a few tensors) are one workgroup's work: it adds
 // and then scales in one launch (fp32, 4 tensors: 16000 elements 5.1 us against

@@ -10,6 +10,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/ssm_linattn.h"
 #include "abi_util.hpp"
 #include "linattn_seqs.hpp"
@@ -27,7 +29,9 @@ using ssm::bf16_t;
 // as the sequence's end state, seg[j] <- x, x <- decay_j x + old seg[j], over
 // the segments in order (reverse: from the last).  One thread per four
 // floats; the loads of four segments are in flight together.  Sequences of
-// one segment have none.
+// one segment have none.  Bound by the states' traffic: 30 us for 2048 states
+// of 64 KB, read and written (8.8 TB/s, since the pass before left much of them
+// in the caches).
 struct CarryArgs {
   Seqs sq;
   int32_t Hv, dkdv, tiles;
@@ -58,11 +62,13 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
   const int64_t slot0 = t0 / L + static_cast<uint32_t>(s);
   float4 x{0.f, 0.f, 0.f, 0.f};
   if (a.s0[rev]) x = *reinterpret_cast<const float4*>(a.s0[rev] + (static_cast<int64_t>(s) * a.Hv + h) * a.dkdv + e);
-  for (int j0 = 0; j0 < nseg; j0 += 4) {
-    float4 u[4];
-    float d[4];
+  // N segments from j0 on, their loads in flight together
+  auto walk = [&](int j0, auto batch) {
+    constexpr int N = decltype(batch)::value;
+    float4 u[N];
+    float d[N];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < N; i++) {
       // the last segment of the walk has no sum: its values are not used
       const int k = j0 + i < nseg - 1 ? j0 + i : 0;
       const int64_t o = (slot0 + (rev ? nseg - 1 - k : k)) * a.Hv + h;
@@ -70,7 +76,7 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
       d[i] = a.decay[rev][o];
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < N; i++) {
       const int k = j0 + i;
       if (k < nseg) {
         const int64_t o = (slot0 + (rev ? nseg - 1 - k : k)) * a.Hv + h;
@@ -81,13 +87,18 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
         x.w = fmaf(d[i], x.w, u[i].w);
       }
     }
-  }
+  };
+  int j0 = 0;
+  for (; j0 + 16 <= nseg; j0 += 16) walk(j0, std::integral_constant<int, 16>{});
+  for (; j0 < nseg; j0 += 4) walk(j0, std::integral_constant<int, 4>{});
 }
 
 // ---------------------------------------------------------------- sums over shared heads and tokens
 
 // out[t][hk][c] = sum over the heads of hk's group, in order, for the rows the
-// sequences cover.  One thread per four channels.
+// sequences cover.  One thread per four channels.  The addends stay fp32, so
+// that many heads cost no digits; reading them bounds it (24 heads of 64,
+// 131072 tokens, dq and dk: 1.6 GB in 387 us, 4.2 TB/s).
 struct GroupArgs {
   const float* part;  // [T][Hv][d]
   void* out;          // [T][Hk][d] in the io type
@@ -124,7 +135,8 @@ __device__ __forceinline__ void group_sum(const Seqs& sq, int32_t Hk, int32_t G,
 // head: for the chunks of each anchor, from the last,
 //   dg_t = (sum over i >= t, forward run) + (sum over j < t, reverse run) + x_c,
 // x_c = e^{G_L} <S, D> at the anchor; then x of the chunk before is x_c plus
-// c's sum over all i less its own sum over all j.
+// c's sum over all i less its own sum over all j.  Bound by the kept states:
+// 68 us for 2 x 2048 of 64 KB (3.9 TB/s).
 struct DecayArgs {
   Seqs sq;
   int32_t Hv, ch, n4;           // tokens of a chunk; float4s of a padded state
@@ -246,7 +258,8 @@ __global__ __launch_bounds__(256) void k_la_decay_sum(int64_t slots, int32_t Hv,
 // h <- e^g h + k v^T, y = scale q h for one row and head and NC of the dv
 // columns per workgroup.  The state is read and written once, 16 bytes a
 // lane; a column of lanes strides the dk rows and their partial sums of y
-// meet in LDS.  Bound by the state's traffic.
+// meet in LDS.  Bound by the state's traffic: 192 rows of 16 heads of 128, 86 us
+// (4.7 TB/s).
 struct StepArgs {
   const void *q, *k, *v;
   int64_t ldq, ldk, ldv, ldy;
@@ -629,7 +642,9 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
 
 template <class T>
 hipError_t run_step(StepArgs a, int64_t rows, hipStream_t st) {
-  // Narrow column tiles while the whole-row form would leave CUs idle.
+  // Narrow column tiles while the whole-row form would leave CUs idle: 16, 64,
+  // 256 rows and heads take 3.7, 4.1, 7.1 us in tiles, 5.9, 6.2, 8.1 whole; 512
+  // and 1024 take 9.9, 22.4 in tiles, 10.1, 21.3 whole.
   const bool narrow = rows * a.Hv < 512;
   a.tiles = narrow ? (a.dv + 31) / 32 : 1;
   const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(a.Hv * a.tiles));
