@@ -25,10 +25,29 @@ using ssm::bf16_t;
 
 // ---------------------------------------------------------------- carry between segments
 
+// A sequence's segments: how many, and the slot of the first.
+struct Walk {
+  int nseg;
+  int64_t slot0;
+};
+
+__device__ __forceinline__ Walk walk_of(const Seqs& sq, int s) {
+  const uint32_t T = static_cast<uint32_t>(sq.T), L = static_cast<uint32_t>(sq.L);
+  const uint32_t n = T / static_cast<uint32_t>(sq.S);
+  auto start = [&](int i) -> uint32_t {
+    if (!sq.start) return n * static_cast<uint32_t>(i);
+    const int32_t v = sq.start[i];
+    return v < 0 ? 0u : static_cast<uint32_t>(v) > T ? T : static_cast<uint32_t>(v);
+  };
+  const uint32_t t0 = start(s), t1 = start(s + 1);
+  if (t1 <= t0) return Walk{0, 0};
+  return Walk{static_cast<int>((t1 - t0 + L - 1) / L), t0 / L + static_cast<uint32_t>(s)};
+}
+
 // Turns the segments' sums into the states entering them, in place: x starts
 // as the sequence's end state, seg[j] <- x, x <- decay_j x + old seg[j], over
 // the segments in order (reverse: from the last).  One thread per four
-// floats; the loads of four segments are in flight together.  Sequences of
+// floats; the loads of up to 16 segments are in flight together.  Sequences of
 // one segment have none.  Bound by the states' traffic: 30 us for 2048 states
 // of 64 KB, read and written (8.8 TB/s, since the pass before left much of them
 // in the caches).
@@ -48,18 +67,10 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
   const int e = (tile * 256 + threadIdx.x) * 4;
   if (e >= a.dkdv) return;
   const int h = blockIdx.y, s = blockIdx.z;
-  const uint32_t T = static_cast<uint32_t>(a.sq.T), L = static_cast<uint32_t>(a.sq.L);
-  const uint32_t n = T / static_cast<uint32_t>(a.sq.S);
-  auto start = [&](int i) -> uint32_t {
-    if (!a.sq.start) return n * static_cast<uint32_t>(i);
-    const int32_t v = a.sq.start[i];
-    return v < 0 ? 0u : static_cast<uint32_t>(v) > T ? T : static_cast<uint32_t>(v);
-  };
-  const uint32_t t0 = start(s), t1 = start(s + 1);
-  if (t1 <= t0) return;
-  const int nseg = static_cast<int>((t1 - t0 + L - 1) / L);
+  const Walk w = walk_of(a.sq, s);
+  const int nseg = w.nseg;
   if (nseg < 2) return;
-  const int64_t slot0 = t0 / L + static_cast<uint32_t>(s);
+  const int64_t slot0 = w.slot0;
   float4 x{0.f, 0.f, 0.f, 0.f};
   if (a.s0[rev]) x = *reinterpret_cast<const float4*>(a.s0[rev] + (static_cast<int64_t>(s) * a.Hv + h) * a.dkdv + e);
   // N segments from j0 on, their loads in flight together
@@ -91,6 +102,70 @@ __global__ __launch_bounds__(256) void k_la_carry(CarryArgs a) {
   int j0 = 0;
   for (; j0 + 16 <= nseg; j0 += 16) walk(j0, std::integral_constant<int, 16>{});
   for (; j0 < nseg; j0 += 4) walk(j0, std::integral_constant<int, 4>{});
+}
+
+// The same with the walk cut into kWalks parts of a workgroup, for many
+// segments of few states: each part sums its segments, takes the state that
+// the parts before it leave, and walks again.  Bound by the latency of a part.
+constexpr int kWalks = 16;
+
+__global__ __launch_bounds__(256) void k_la_carry_split(CarryArgs a) {
+  constexpr int kCols = 256 / kWalks;
+  __shared__ float4 sums[kWalks][kCols];
+  __shared__ float decays[kWalks];
+  const bool rev = blockIdx.x >= static_cast<unsigned>(a.tiles);
+  const int tile = rev ? blockIdx.x - a.tiles : blockIdx.x;
+  float* const seg = a.seg[rev];
+  if (!seg) return;
+  const int h = blockIdx.y, s = blockIdx.z;
+  const Walk w = walk_of(a.sq, s);
+  if (w.nseg < 2) return;
+  const int col = threadIdx.x % kCols, part = threadIdx.x / kCols;
+  const int e = (tile * kCols + col) * 4;  // a state is a multiple of kCols * 4 floats
+  const int n = (w.nseg + kWalks - 1) / kWalks;
+  const int k0 = part * n, k1 = k0 + n < w.nseg ? k0 + n : w.nseg;
+  auto slot = [&](int k) { return (w.slot0 + (rev ? w.nseg - 1 - k : k)) * a.Hv + h; };
+  auto walk = [&](float4 x, bool put) {
+    float d = 1.0f;
+    for (int j0 = k0; j0 < k1; j0 += 8) {
+      float4 u[8];
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        // the last segment of the sequence's walk has no sum: its values are not used
+        const int k = j0 + i < k1 && j0 + i < w.nseg - 1 ? j0 + i : 0;
+        u[i] = *reinterpret_cast<const float4*>(seg + slot(k) * a.dkdv + e);
+        f[i] = a.decay[rev][slot(k)];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        if (j0 + i < k1) {
+          if (put) *reinterpret_cast<float4*>(seg + slot(j0 + i) * a.dkdv + e) = x;
+          x.x = fmaf(f[i], x.x, u[i].x);
+          x.y = fmaf(f[i], x.y, u[i].y);
+          x.z = fmaf(f[i], x.z, u[i].z);
+          x.w = fmaf(f[i], x.w, u[i].w);
+          d *= f[i];
+        }
+      }
+    }
+    sums[part][col] = x;
+    if (col == 0) decays[part] = d;
+  };
+  walk(float4{0.f, 0.f, 0.f, 0.f}, false);
+  __syncthreads();
+  float4 x{0.f, 0.f, 0.f, 0.f};
+  if (a.s0[rev]) x = *reinterpret_cast<const float4*>(a.s0[rev] + (static_cast<int64_t>(s) * a.Hv + h) * a.dkdv + e);
+  for (int p = 0; p < part; p++) {
+    const float4 u = sums[p][col];
+    const float d = decays[p];
+    x.x = fmaf(d, x.x, u.x);
+    x.y = fmaf(d, x.y, u.y);
+    x.z = fmaf(d, x.z, u.z);
+    x.w = fmaf(d, x.w, u.w);
+  }
+  __syncthreads();
+  walk(x, true);
 }
 
 // ---------------------------------------------------------------- sums over shared heads and tokens
@@ -524,7 +599,16 @@ hipError_t carry_states(const ssm_linattn_dims* d, Args a, const Run& fwd, const
   c.sq = a.sq;
   c.Hv = d->Hv;
   c.dkdv = a.dkdv;
-  c.tiles = (a.dkdv / 4 + 255) / 256;
+  // Long walks of few states leave the chip idle unless they are cut; with
+  // many states the second read costs more.  Forward, whole and cut: 65536
+  // tokens, 1, 4, 16 heads of 128: 113, 150, 497 us and 60, 124, 497; 131072
+  // tokens, 1, 4, 24 heads of 64: 124, 127, 652 and 49, 102, 650; 4096 tokens,
+  // 16 heads of 128: 58 and 65; 16 or 8 segments, 4 heads of 64: 17.7 and 17.7,
+  // 16.4 and 17.0.
+  const int64_t tiles = (a.dkdv / 4 + 255) / 256;
+  const int64_t most = (longest(d, a.sq.start != nullptr) + a.sq.L - 1) / a.sq.L;
+  const bool split = most > kWalks && tiles * d->Hv * d->S <= 64;
+  c.tiles = static_cast<int32_t>(split ? a.dkdv / 4 / (256 / kWalks) : tiles);
   c.s0[0] = h0; c.s0[1] = dhT;
   for (int i = 0; i < 2; i++) {
     c.seg[i] = w.seg[i];
@@ -532,7 +616,8 @@ hipError_t carry_states(const ssm_linattn_dims* d, Args a, const Run& fwd, const
   }
   const dim3 grid(static_cast<unsigned>(c.tiles * (w.seg[1] ? 2 : 1)), static_cast<unsigned>(d->Hv),
                   static_cast<unsigned>(d->S));
-  k_la_carry<<<grid, 256, 0, st>>>(c);
+  if (split) k_la_carry_split<<<grid, 256, 0, st>>>(c);
+  else k_la_carry<<<grid, 256, 0, st>>>(c);
   return hipGetLastError();
 }
 

@@ -224,3 +224,24 @@ def test_bf16_rounded_once(agm, lens, Hk, Hv, dk, dv, states):
         for o in out:
             over = (o.double().cpu() - refs[0][n]).abs() - 2.0 ** -8 * refs[0][n].abs() - 2.0 ** -15 * refs[1][n]
             assert float(over.max()) <= 0, (n, float(over.max()))
+
+
+@pytest.mark.parametrize("io,lens,Hk,Hv,dk,dv", [
+    ("f32", [1700], 1, 1, 8, 24), ("f32", [1030, 0, 131, 1, 64], 2, 2, 40, 16), ("bf16", [2300], 1, 2, 64, 32)])
+def test_long_walks_of_few_states(agm, io, lens, Hk, Hv, dk, dv):
+    """More segments than parts of a carried walk, not a multiple of them, beside
+    sequences of one segment and none; decays slow enough to reach across them."""
+    spans = spans_of(lens, 0)
+    T = spans[-1][1]
+    d = ref.inputs(61, T, Hk, Hv, dk, dv, io, S=len(lens), states=True)
+    d["g"] = d["g"] * 0.05
+    want, ends = ref.forward(d["q"], d["k"], d["v"], d["g"], spans, 0.5, d["h0"])
+    gw, _ = ref.gradient(d["q"], d["k"], d["v"], d["g"], d["dy"], spans, 0.5, d["h0"], d["dhT"])
+    t = device_inputs(d, io)
+    off = starts(spans)
+    y, hT = agm.linattn_forward(t["q"], t["k"], t["v"], t["g"], seq_start=off, h0=t["h0"], scale=0.5, want_state=True)
+    got = agm.linattn_grad(t["q"], t["k"], t["v"], t["g"], t["dy"], seq_start=off, h0=t["h0"], dhT=t["dhT"], scale=0.5)
+    check("y", y.cpu(), want, io, "walks")
+    check("hT", hT.cpu(), ends, io, "walks")
+    for n in got:
+        check(n, got[n].cpu(), gw[n], io, "walks")
