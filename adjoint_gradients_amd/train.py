@@ -70,7 +70,7 @@ def add_norm(r, y, norm_scale, eps=1e-5, r_out=None, x=None, rinv=None, io=None,
     else:
         _dense(x, "x", shape, device, dt)
     if rinv is None:
-        rinv = torch.empty(shape[:-1], dtype=_F32, device=r.device)
+        rinv = r.new_empty(T if len(shape) == 2 else shape[:-1])
     else:
         _dense(rinv, "rinv", shape[:-1], device, _F32)
     _check(lib.ssm_add_norm(T, P, _IO[dt], rp, yp, gp, eps, r_out.data_ptr(), x.data_ptr(), rinv.data_ptr(),
@@ -114,14 +114,26 @@ def add_norm_grad(r_out, rinv, norm_scale, dx, dr_out=None, dr=None, want_scale=
 
 def _addresses(ts, name: str, device, dtype):
     """The addresses of contiguous tensors of one dtype on one device."""
-    out = []
+    try:
+        if all([t.get_device() == device and t.dtype is dtype and t.is_contiguous() for t in ts]):
+            return [t.data_ptr() for t in ts]
+    except AttributeError:
+        pass  # not a tensor: refused below
     for t in ts:
-        if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dtype:
-            _gpu(t, name, device, dtype)
+        _gpu(t, name, device, dtype)
         if not t.is_contiguous():
             _bad(f"{name}: must be contiguous")
-        out.append(t.data_ptr())
-    return out
+
+
+def _check_outputs(pi, po, ts):
+    """Refuses an output given twice or that is another gradient (empty tensors share the null address)."""
+    full = [i for i, t in enumerate(ts) if t.numel()]
+    source = {pi[i]: i for i in full}
+    if len({po[i] for i in full}) != len(full):
+        _bad("clip_grads: an output is given twice")
+    for i in full:
+        if source.get(po[i], i) != i:
+            _bad("clip_grads: an output is another gradient")
 
 
 def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
@@ -161,14 +173,12 @@ def clip_grads(grads, max_norm, out=None, norm=None, ws=None, stream=None):
         if len(out) != n:
             _bad(f"clip_grads: {len(out)} outputs for {n} gradients")
         po = _addresses(out, "an output", device, dt)
-        source = {p: i for i, (p, t) in enumerate(zip(pi, ts)) if t.numel()}
-        if len({p for p, t in zip(po, ts) if t.numel()}) != sum(1 for t in ts if t.numel()):
-            _bad("clip_grads: an output is given twice")
-        for i, (o, t) in enumerate(zip(out, ts)):
-            if t.numel() and source.get(po[i], i) != i:
-                _bad("clip_grads: an output is another gradient")
+        for o, t in zip(out, ts):
             if o.shape != t.shape:
                 _bad(f"an output: shape {tuple(o.shape)}, expected {tuple(t.shape)}")
+        used = set(po)
+        if len(used) != n or not used.isdisjoint(pi):
+            _check_outputs(pi, po, ts)
     ptrs, counts = _VP * n, _I64 * n
     ns = counts(*[t.numel() for t in ts])
     nbytes = lib.ssm_clip_grads_workspace_bytes(n, ns)
