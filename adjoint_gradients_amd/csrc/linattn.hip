@@ -583,7 +583,7 @@ Run make_run(const Op& q, const Op& k, const Op& v, float qs, float ks) {
 }
 
 // The segments' entering states, for the directions in use (runs of the aggregate kernel).
-hipError_t carry_states(const ssm_linattn_dims* d, Args a, const Run& fwd, const Run& rev, const Ws& w,
+hipError_t carry_states(Kernel sums, const ssm_linattn_dims* d, Args a, const Run& fwd, const Run& rev, const Ws& w,
                         const float* h0, const float* dhT, hipStream_t st) {
   a.run[0] = fwd;
   a.run[1] = rev;
@@ -593,7 +593,7 @@ hipError_t carry_states(const ssm_linattn_dims* d, Args a, const Run& fwd, const
     a.run[i].sm = d->dv;
     a.run[i].sn = 1;
   }
-  hipError_t e = launch(kAggregate, d, a, st);
+  hipError_t e = launch(sums, d, a, st);
   if (e != hipSuccess) return e;
   CarryArgs c{};
   c.sq = a.sq;
@@ -631,7 +631,7 @@ hipError_t run_forward(const ssm_linattn_dims* d, const ssm_linattn_in* in, void
   Args a = base_args(d, in, p);
   Run r = make_run(q, k, v, d->scale, 1.0f);
   if (p.split) {
-    hipError_t e = carry_states(d, a, r, Run{}, w, in->h0, nullptr, st);
+    hipError_t e = carry_states(hT ? kAggregate : kAggregateOut, d, a, r, Run{}, w, in->h0, nullptr, st);
     if (e != hipSuccess) return e;
   }
   r.s0 = in->h0;
@@ -658,7 +658,8 @@ hipError_t run_grad(const ssm_linattn_dims* d, const ssm_linattn_in* in, const v
   if (p.split) {
     const Run fwd = p.need_s ? make_run(k, k, v, 1.0f, 1.0f) : Run{};
     const Run rev = p.need_d ? make_run(q, q, o, 1.0f, d->scale) : Run{};
-    if ((e = carry_states(d, a, fwd, rev, w, in->h0, dhT, st)) != hipSuccess) return e;
+    const Kernel sums = p.dg || g->dh0 ? kAggregate : kAggregateOut;
+    if ((e = carry_states(sums, d, a, fwd, rev, w, in->h0, dhT, st)) != hipSuccess) return e;
   }
   const int64_t part_ld = static_cast<int64_t>(d->Hv) * d->dk;
   // dq: state S^T, entered by h0

@@ -57,6 +57,7 @@ enum Kernel {
   kForward,    // run 0: y
   kForwardState,  // the same where the final state is an output too
   kAggregate,  // run 0: the segments' state sums, forward in time; run 1: in reverse
+  kAggregateOut,  // the same where the states reach only outputs of the io type
   kGradPlain,  // runs 0, 1, 2: dq, dk (and the adjoint of h0), dv
   kGradDecay   // the same with the decay gradient's terms
 };

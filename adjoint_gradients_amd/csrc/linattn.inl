@@ -50,6 +50,8 @@
 // few tokens, whose sums do not average the roundings, were off by up to 3.5e-3
 // where the output's rounding is 1.5e-3; the second part costs the forward
 // pass of 65536 tokens, 16 heads of 128, 2% (475 -> 484 us), its gradient 2%.
+// Three parts in the segments' sums where two do: 590 us against 556 for 131072
+// tokens, 24 heads of 64.
 #include "linattn_seqs.hpp"
 #include "ssm_common.hpp"
 
@@ -904,7 +906,7 @@ __device__ __forceinline__ Work work_of(const Args& a) {
 // for (the LDS does too).
 constexpr int wgs_per_cu(int dk, int dv, int kind) {
   const int n = dk * dv > 64 * 64 ? 2 : 3;
-  return kind == kAggregate ? n + 1 : n;
+  return kind == kAggregate || kind == kAggregateOut ? n + 1 : n;
 }
 
 // Kinds: kGrad... with PT the type of dq and dk, float where the value heads
@@ -918,9 +920,10 @@ __global__ __launch_bounds__(kThreads, wgs_per_cu(DK, DV, KIND)) void k_linattn(
     run<T, T, DK, DV, false, kOut, kOutParts>(a, a.run[0], w.slot, w.h, smem_la);
   } else if constexpr (KIND == kForwardState) {
     run<T, T, DK, DV, false, kOut, kParts>(a, a.run[0], w.slot, w.h, smem_la);
-  } else if constexpr (KIND == kAggregate) {
-    if (w.z == 0) run<T, T, DK, DV, false, kAgg, kParts>(a, a.run[0], w.slot, w.h, smem_la);
-    else run<T, T, DK, DV, true, kAgg, kParts>(a, a.run[1], w.slot, w.h, smem_la);
+  } else if constexpr (KIND == kAggregate || KIND == kAggregateOut) {
+    constexpr int P = KIND == kAggregate ? kParts : kOutParts;
+    if (w.z == 0) run<T, T, DK, DV, false, kAgg, P>(a, a.run[0], w.slot, w.h, smem_la);
+    else run<T, T, DK, DV, true, kAgg, P>(a, a.run[1], w.slot, w.h, smem_la);
   } else {
     constexpr bool dg = KIND == kGradDecay;
     if (w.z == 0) run<T, PT, DV, DK, false, dg ? kOutFwdDg : kOut, dg ? kParts : kOutParts>(a, a.run[0], w.slot, w.h, smem_la);
@@ -934,7 +937,7 @@ constexpr int max2(int a, int b) { return a > b ? a : b; }
 template <class T, int DK, int DV, int KIND>
 constexpr int lds_bytes() {
   if (KIND == kForward || KIND == kForwardState) return Lds<T, DK, DV, kOut>::bytes;
-  if (KIND == kAggregate) return Lds<T, DK, DV, kAgg>::bytes;
+  if (KIND == kAggregate || KIND == kAggregateOut) return Lds<T, DK, DV, kAgg>::bytes;
   if (KIND == kGradDecay) return max2(Lds<T, DV, DK, kOutFwdDg>::bytes, Lds<T, DK, DV, kOut>::bytes);
   return max2(Lds<T, DV, DK, kOut>::bytes, Lds<T, DK, DV, kOut>::bytes);
 }
@@ -958,7 +961,10 @@ template <class T, int DK, int DV>
 hipError_t launch_kind(Kernel k, const Args& a, hipStream_t st) {
   if (k == kForward) return launch_one<T, T, DK, DV, kForward>(a, st);
   if (k == kForwardState) return launch_one<T, T, DK, DV, kForwardState>(a, st);
-  if (k == kAggregate) return launch_one<T, T, DK, DV, kAggregate>(a, st);
+  if constexpr (Cfg<T>::kBf) {  // fp32 has no parts
+    if (k == kAggregateOut) return launch_one<T, T, DK, DV, kAggregateOut>(a, st);
+  }
+  if (k == kAggregate || k == kAggregateOut) return launch_one<T, T, DK, DV, kAggregate>(a, st);
   if (a.sum_heads)
     return k == kGradDecay ? launch_one<T, float, DK, DV, kGradDecay>(a, st)
                            : launch_one<T, float, DK, DV, kGradPlain>(a, st);
