@@ -103,7 +103,7 @@ def test_linattn_refuses_the_rest(agm):
 
 def test_linattn_workspace(agm):
     # few tokens for one sequence: nothing to split, nothing needed
-    assert size(agm, dims(agm, T=200)) == (OK, 0)
+    assert size(agm, dims(agm, T=128)) == (OK, 0)
     rc, n = size(agm, dims(agm, T=65536))
     assert rc == OK and n > 0
     # a long sequence needs its segments' states, however few heads; refused when short or unaligned
