@@ -48,8 +48,8 @@ __device__ __forceinline__ Walk walk_of(const Seqs& sq, int s) {
 // as the sequence's end state, seg[j] <- x, x <- decay_j x + old seg[j], over
 // the segments in order (reverse: from the last).  One thread per four
 // floats; the loads of up to 16 segments are in flight together.  Sequences of
-// one segment have none.  Bound by the states' traffic: 30 us for 2048 states
-// of 64 KB, read and written (8.8 TB/s, since the pass before left much of them
+// one segment have none.  Bound by the states' traffic: 32 us for 2048 states
+// of 64 KB, read and written (8.4 TB/s, since the pass before left much of them
 // in the caches).
 struct CarryArgs {
   Seqs sq;

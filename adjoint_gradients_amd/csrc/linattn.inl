@@ -35,11 +35,11 @@
 // What bounds it (bf16, 65536 tokens, 16 heads of 128): the pass that sums the
 // segments runs at memory speed (forward 131 us for 0.54 GB of k and v and
 // 0.13 GB of states), the forward run nearly so (270 us for 1.07 GB of rows).
-// The gradient's three runs (1.17 ms, half of it what their 3 GB would take)
+// The gradient's three runs (1.19 ms, half of it what their 3 GB would take)
 // are bound by the chain scores - state - product - update of a chunk, which
-// two workgroups a CU hide in part: the matrix units do 0.57 PFLOP/s, half of
+// two workgroups a CU hide in part: the matrix units do 0.56 PFLOP/s, half of
 // what a large library product reaches.  64-wide heads (24 of them, 131072
-// tokens, one head of q and k: 133 us and 345 us for 0.40 and 0.81 GB) are
+// tokens, one head of q and k: 124 us and 325 us for 0.40 and 0.81 GB) are
 // bound by the same chain, with vector instructions busy two fifths of the time.
 //
 // Rounding: products are bf16 x bf16 summed in fp32 (or fp32 throughout).  An
