@@ -333,8 +333,9 @@ __global__ __launch_bounds__(256) void k_la_decay_sum(int64_t slots, int32_t Hv,
 // h <- e^g h + k v^T, y = scale q h for one row and head and NC of the dv
 // columns per workgroup.  The state is read and written once, 16 bytes a
 // lane; a column of lanes strides the dk rows and their partial sums of y
-// meet in LDS.  Bound by the state's traffic: 192 rows of 16 heads of 128, 86 us
-// (4.7 TB/s).
+// meet in LDS.  Bound by the state's traffic: 192 rows of 16 heads of 128, 76 us
+// (5.3 TB/s).  STREAM: past the caches, for states that they will not hold
+// until the next token.
 struct StepArgs {
   const void *q, *k, *v;
   int64_t ldq, ldk, ldv, ldy;
@@ -346,7 +347,21 @@ struct StepArgs {
   float scale;
 };
 
-template <class T, int NC>
+typedef __attribute__((__vector_size__(4 * sizeof(float)))) float f32x4;
+
+template <bool STREAM>
+__device__ __forceinline__ float4 state_load(const float* p) {
+  const f32x4* const v = reinterpret_cast<const f32x4*>(p);
+  return __builtin_bit_cast(float4, STREAM ? __builtin_nontemporal_load(v) : *v);
+}
+template <bool STREAM>
+__device__ __forceinline__ void state_store(float* p, float4 x) {
+  f32x4* const v = reinterpret_cast<f32x4*>(p);
+  if (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(f32x4, x), v);
+  else *v = __builtin_bit_cast(f32x4, x);
+}
+
+template <class T, int NC, bool STREAM>
 __global__ __launch_bounds__(256) void k_la_step(StepArgs a) {
   constexpr int CG = NC / 4;        // lanes across the columns
   constexpr int RG = 256 / CG;      // lanes down the rows
@@ -363,7 +378,7 @@ __global__ __launch_bounds__(256) void k_la_step(StepArgs a) {
 #pragma unroll
   for (int i = 0; i < NR; i++) {
     const int m = rg + RG * i;
-    if (in && m < a.dk) s[i] = *reinterpret_cast<const float4*>(st + m * a.dv);
+    if (in && m < a.dk) s[i] = state_load<STREAM>(st + m * a.dv);
   }
   const int hk = h / a.G;
   if (threadIdx.x < static_cast<unsigned>(a.dk)) {
@@ -392,7 +407,7 @@ __global__ __launch_bounds__(256) void k_la_step(StepArgs a) {
       s[i].y = fmaf(w, s[i].y, k * v.y);
       s[i].z = fmaf(w, s[i].z, k * v.z);
       s[i].w = fmaf(w, s[i].w, k * v.w);
-      *reinterpret_cast<float4*>(st + m * a.dv) = s[i];
+      state_store<STREAM>(st + m * a.dv, s[i]);
       y.x = fmaf(q, s[i].x, y.x);
       y.y = fmaf(q, s[i].y, y.y);
       y.z = fmaf(q, s[i].z, y.z);
@@ -734,8 +749,14 @@ hipError_t run_step(StepArgs a, int64_t rows, hipStream_t st) {
   const bool narrow = rows * a.Hv < 512;
   a.tiles = narrow ? (a.dv + 31) / 32 : 1;
   const dim3 grid(static_cast<unsigned>(rows), static_cast<unsigned>(a.Hv * a.tiles));
-  if (narrow) k_la_step<T, 32><<<grid, 256, 0, st>>>(a);
-  else k_la_step<T, 128><<<grid, 256, 0, st>>>(a);
+  // From a quarter of the 256 MB cache on, the states of a few layers evict one
+  // another.  Five of them in turn, 16 heads of 128, cached and streamed: 192
+  // rows 87 and 76 us, 64 rows (67 MB) 35 and 26, 32 rows 13.4 and 13.9; one
+  // alone: 60 and 75, 21.5 and 22.8, 9.9 and 11.8.
+  const bool stream = rows * a.Hv * a.dk * a.dv * 4 >= (int64_t(64) << 20);
+  if (narrow) k_la_step<T, 32, false><<<grid, 256, 0, st>>>(a);
+  else if (stream) k_la_step<T, 128, true><<<grid, 256, 0, st>>>(a);
+  else k_la_step<T, 128, false><<<grid, 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

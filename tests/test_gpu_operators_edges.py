@@ -245,3 +245,18 @@ def test_long_walks_of_few_states(agm, io, lens, Hk, Hv, dk, dv):
     check("hT", hT.cpu(), ends, io, "walks")
     for n in got:
         check(n, got[n].cpu(), gw[n], io, "walks")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_step_of_many_states(agm, io):
+    """States larger than the caches keep, in widths that fill no tile; a second step finds the first one's."""
+    B, Hk, Hv, dk, dv = 43, 8, 32, 120, 104
+    d = ref.inputs(62, B, Hk, Hv, dk, dv, io, S=B, states=True)
+    t = device_inputs(d, io)
+    q, k = (d[n].repeat_interleave(Hv // Hk, dim=1) for n in ("q", "k"))
+    st, h = t["h0"].clone(), d["h0"]
+    for _ in range(2):
+        h = torch.exp(d["g"])[..., None, None] * h + k[..., None] * d["v"][:, :, None, :]
+        y = agm.linattn_step(t["q"], t["k"], t["v"], t["g"], st, scale=0.5)
+        check("y", y.cpu(), 0.5 * (q[..., None] * h).sum(2), io, "many states")
+    assert ref.rms_err(st.cpu(), h) <= 2.0 ** -22  # two steps of two fp32 roundings each
