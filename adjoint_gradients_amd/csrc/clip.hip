@@ -7,7 +7,7 @@
 // whose workgroups first adds the partial sums in the same fixed order.  The
 // scaling walks the tensors from the end, so that what the first pass read
 // last, and the caches still hold, is read first.  51.5 million fp32 elements in
-// 60 tensors: 42 us and 68 us (0.21 GB read; 0.21 read and 0.21 written).
+// 60 tensors: 103 us, of it 40 the sum (0.21 GB at 5.1 TB/s).
 //
 // Few elements (kSmall, in a few tensors) are one workgroup's work: it adds
 // and then scales in one launch (fp32, 4 tensors: 16000 elements 5.1 us against
@@ -91,6 +91,19 @@ template <> struct Vec<bf16_t> {
     return uint4{w[0], w[1], w[2], w[3]};
   }
 };
+
+typedef __attribute__((__vector_size__(4 * sizeof(uint32_t)))) uint32_t u32x4;
+template <bool STREAM>
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  const u32x4* const q = reinterpret_cast<const u32x4*>(p);
+  return __builtin_bit_cast(uint4, STREAM ? __builtin_nontemporal_load(q) : *q);
+}
+template <bool STREAM>
+__device__ __forceinline__ void store16(uint4* p, uint4 v) {
+  u32x4* const q = reinterpret_cast<u32x4*>(p);
+  if (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), q);
+  else *q = __builtin_bit_cast(u32x4, v);
+}
 
 __device__ __forceinline__ double wg_sum(double s, double* red) {
 #pragma unroll
@@ -188,7 +201,9 @@ __global__ __launch_bounds__(1024) void k_clip_small(Table t, float max_norm, in
   }
 }
 
-template <class T>
+// STREAM: past the caches, so that the outputs leave them to the inputs that
+// the sum has just read.
+template <class T, bool STREAM>
 __global__ __launch_bounds__(256) void k_clip_scale(Table t, const double* __restrict__ part, int nparts,
                                                    float max_norm, int scale, float* __restrict__ norm) {
   __shared__ double red[4];
@@ -208,14 +223,14 @@ __global__ __launch_bounds__(256) void k_clip_scale(Table t, const double* __res
     if (p.n == kBlock) {
       uint4 u[U];
 #pragma unroll
-      for (int j = 0; j < U; j++) u[j] = reinterpret_cast<const uint4*>(src)[threadIdx.x + 256 * j];
+      for (int j = 0; j < U; j++) u[j] = load16<STREAM>(reinterpret_cast<const uint4*>(src) + threadIdx.x + 256 * j);
 #pragma unroll
       for (int j = 0; j < U; j++) {
         float f[N];
         Vec<T>::get(u[j], f);
 #pragma unroll
         for (int e = 0; e < N; e++) f[e] = clip ? f[e] * c : f[e];
-        reinterpret_cast<uint4*>(dst)[threadIdx.x + 256 * j] = Vec<T>::put(f);
+        store16<STREAM>(reinterpret_cast<uint4*>(dst) + threadIdx.x + 256 * j, Vec<T>::put(f));
       }
     } else {
       for (int e = threadIdx.x; e < p.n; e += 256) {
@@ -271,11 +286,16 @@ hipError_t run_clip(int32_t count, const void* const* in, void* const* out, cons
     if (e != hipSuccess) return e;
     nparts += static_cast<int>(g);
   }
+  // Gradients of three quarters of the 256 MB cache or more leave no room for
+  // what reads the outputs next.  fp32, cached and streamed, alone and with a
+  // pass over the outputs behind: 96 MB 61 and 53, 106 and 110 us; 160 MB 100 and
+  // 82, 161 and 171; 208 MB 128 and 105, 214 and 215; 320 MB 194 and 157, 322 and 313.
+  const bool stream = total * static_cast<int64_t>(sizeof(T)) >= (int64_t(192) << 20);
   const int32_t last = static_cast<int32_t>((launches_for(count) - 1) * kTable);
   for (int32_t i = last; i >= 0; i -= kTable) {
     const Table t = table_of(i, count, in, out, n);
-    k_clip_scale<T><<<out ? wgs_for(t) : 1u, 256, 0, st>>>(t, part, nparts, max_norm, out ? 1 : 0,
-                                                           i == last ? norm : nullptr);
+    const auto k = stream ? k_clip_scale<T, true> : k_clip_scale<T, false>;
+    k<<<out ? wgs_for(t) : 1u, 256, 0, st>>>(t, part, nparts, max_norm, out ? 1 : 0, i == last ? norm : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !out) return e;
   }

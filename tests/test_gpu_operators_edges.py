@@ -260,3 +260,22 @@ def test_step_of_many_states(agm, io):
         y = agm.linattn_step(t["q"], t["k"], t["v"], t["g"], st, scale=0.5)
         check("y", y.cpu(), 0.5 * (q[..., None] * h).sum(2), io, "many states")
     assert ref.rms_err(st.cpu(), h) <= 2.0 ** -22  # two steps of two fp32 roundings each
+
+
+@pytest.mark.parametrize("io,n", [("f32", 51_000_003), ("bf16", 101_000_005)])
+def test_clip_more_than_the_caches(agm, io, n):
+    """Gradients that the caches do not hold, into other tensors and in place: every element is the
+    input times one factor, rounded once (half a step), the factor off by 2^-23 (its own rounding and the norm's)."""
+    t = torch.randn(n, device="cuda", generator=torch.Generator("cuda").manual_seed(9)).to(IO[io])
+    ts = [t[: n // 3].clone(), t[n // 3: n // 3].clone(), t[n // 3:].clone()]
+    total = float(sum(x.double().square().sum() for x in ts)) ** 0.5
+    out = [torch.empty_like(x) for x in ts]
+    norm = agm.clip_grads(ts, total / 3, out=out)
+    assert abs(float(norm) - total) <= 2.0 ** -23 * total
+    again = [x.clone() for x in ts]
+    agm.clip_grads(again, total / 3)
+    tol = torch.finfo(IO[io]).eps / 2 + 2.0 ** -23
+    for x, o, a in zip(ts, out, again):
+        assert torch.equal(o, a)
+        want = x.double() / 3
+        assert bool(((o.double() - want).abs() <= tol * want.abs()).all())
